@@ -1,7 +1,7 @@
 """Low-bit all-reduce activation codec for AMD Instinct MI355X (gfx950).
 
-A thin ctypes binding over the C ABI in `include/fc.h` (libfc.so, built from
-`csrc/` by `build.py`). Every step of the codec runs in the library's HIP
+A thin ctypes binding over the C ABI in `include/fc.h` and `include/fc/layer.h`
+(libfc.so, built from `csrc/` by `build.py`). Every step of the codec runs in the library's HIP
 kernels; this module only checks tensor metadata, allocates outputs with
 torch on the input's device, and passes raw device pointers and the current
 HIP stream. There is no fallback: if the library cannot be loaded, calls
@@ -14,6 +14,7 @@ All-Gather, dequantize after it (Figure 5, right; groups as in Figure 4).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -27,6 +28,9 @@ __all__ = [
     "fc_sum_uncompressed", "fc_dequantize_residual", "fc_linear_quantize", "workspace_views",
     "fc_allreduce_emulated_noalloc", "NOALLOC_SCRATCH_BYTES",
     "EXPORTED_SYMBOLS",
+    "fc_residual_norm", "fc_dequantize_residual_norm", "fc_allreduce_emulated_norm",
+    "fc_quantize_mxfp4", "fc_dequantize_mxfp4", "fc_matmul_mxfp4", "fc_linear_mxfp4",
+    "fc_linear_mxfp4_workspace_bytes", "LAYER_SYMBOLS",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +45,12 @@ EXPORTED_SYMBOLS = (
     "fc_workspace_bytes_mixed", "fc_workspace_layout_mixed",
     "fc_dequantize_residual", "fc_allreduce_emulated_residual", "fc_linear_quantize",
     "fc_allreduce_emulated_noalloc",
+)
+# the operators of include/fc/layer.h
+LAYER_SYMBOLS = (
+    "fc_residual_norm", "fc_dequantize_residual_norm", "fc_allreduce_emulated_norm",
+    "fc_quantize_mxfp4", "fc_dequantize_mxfp4", "fc_matmul_mxfp4", "fc_linear_mxfp4",
+    "fc_linear_mxfp4_workspace_bytes",
 )
 # FC_NOALLOC_SCRATCH_BYTES of include/fc.h: the payload scratch the library holds per device
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -83,6 +93,21 @@ def lib() -> ctypes.CDLL:
                       L.fc_dequantize_residual, L.fc_allreduce_emulated_residual,
                       L.fc_allreduce_emulated_noalloc):
                 f.restype = I
+            F = ctypes.c_float
+            norm = [P, P, I, P, F, F, F, P, P]   # w_post, gate, gate_tokens, w_pre, scales, eps, h, y
+            L.fc_residual_norm.argtypes = [P, P, I, I, I, *norm, P]
+            L.fc_dequantize_residual_norm.argtypes = [P, P, P, I, I, I, I, I, P, *norm, P]
+            L.fc_allreduce_emulated_norm.argtypes = [P, I, I, I, I, I, I, I, P, *norm, P, Z, P]
+            L.fc_quantize_mxfp4.argtypes = [P, I, I, I, I, P, P, P]
+            L.fc_dequantize_mxfp4.argtypes = [P, P, I, I, I, I, P, P]
+            L.fc_matmul_mxfp4.argtypes = [P, P, P, P, I, I, I, I, I, P, P]
+            L.fc_linear_mxfp4.argtypes = [P, P, P, I, I, I, I, I, P, P, Z, P]
+            for f in (L.fc_residual_norm, L.fc_dequantize_residual_norm, L.fc_allreduce_emulated_norm,
+                      L.fc_quantize_mxfp4, L.fc_dequantize_mxfp4, L.fc_matmul_mxfp4,
+                      L.fc_linear_mxfp4):
+                f.restype = I
+            L.fc_linear_mxfp4_workspace_bytes.argtypes = [I, I, I]
+            L.fc_linear_mxfp4_workspace_bytes.restype = Z
             L.fc_workspace_bytes_mixed.argtypes = [I, I, I, I, I, I]
             L.fc_workspace_bytes_mixed.restype = Z
             L.fc_workspace_layout_mixed.argtypes = [I, I, I, I, I, I, ctypes.POINTER(Z),
@@ -387,3 +412,243 @@ def workspace_views(workspace: torch.Tensor, R: int, T: int, H: int, bits: int, 
         raw = workspace[off:off + size]
         out[name] = raw.view(torch.uint16).view(shape) if name[0] in "sz" else raw.view(shape)
     return out
+
+
+# --- transformer-block operators (include/fc/layer.h) ------------------------
+
+def _on(device):
+    """The device's own context: the library launches on the current device. (A
+    no-op object when it is the current one already.)"""
+    return torch.cuda.device(device) if device.index not in (None, torch.cuda.current_device()) \
+        else contextlib.nullcontext()
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream` (None: torch's current one). It belongs to
+    that stream: memory that other streams still use cannot come back in it, and it is
+    not handed on before the call's work is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _like(t: torch.Tensor, name: str, shape, dtype, device) -> None:
+    """An operand of exactly this shape and dtype on `device`."""
+    _dev_tensor(t, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
+
+
+def _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream):
+    """Checks what the block-norm calls share; -> (dtype code, gate_tokens, h, y)."""
+    dev, dt = residual.device, residual.dtype
+    code = _dt(residual, "residual")
+    _like(residual, "residual", (T, H), dt, dev)
+    if w_post is not None:
+        _like(w_post, "w_post", (H,), dt, dev)
+    if w_pre is not None:
+        _like(w_pre, "w_pre", (H,), dt, dev)
+    if gate is not None:
+        if gate_tokens is None:
+            gate_tokens = max(T, 1) if gate.dim() == 1 else 1
+        if gate_tokens < 1:
+            raise ValueError(f"gate_tokens must be at least 1, not {gate_tokens}")
+        rows = -(-T // gate_tokens)
+        _like(gate, "gate", (H,) if gate.dim() == 1 and rows <= 1 else (rows, H), dt, dev)
+    if h is None:
+        h = _empty((T, H), dt, dev, stream)
+    _like(h, "h", (T, H), dt, dev)
+    if w_pre is None:
+        if y is not None:
+            raise ValueError("y needs w_pre")
+    else:
+        if y is None:
+            y = _empty((T, H), dt, dev, stream)
+        _like(y, "y", (T, H), dt, dev)
+    return code, gate_tokens or 1, h, y
+
+
+def fc_residual_norm(x: torch.Tensor, residual: torch.Tensor, w_post=None, w_pre=None, gate=None,
+                     gate_tokens: int | None = None, eps: float = 1e-5, res_scale: float = 1.0,
+                     out_scale: float = 1.0, h=None, y=None, stream=None):
+    """Block norms of a block output x [T, H] and the residual stream [T, H] (fp16/bf16):
+        h = res_scale * residual + out_scale * gate * post_norm(x),  y = pre_norm(h)
+    -> (h, y), y None without w_pre. w_post and w_pre [H] are RMS-norm weights; without
+    w_post x is not normed. gate: [H], or a row for every gate_tokens consecutive tokens
+    (default: a row per token). `h` may be `residual` itself (in-place update)."""
+    _dev_tensor(residual, "residual")
+    if residual.dim() != 2:
+        raise ValueError("residual must be [T, H]")
+    T, H = residual.shape
+    dev = residual.device
+    _like(x, "x", (T, H), residual.dtype, dev)
+    code, gate_tokens, h, y = _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
+    with _on(dev):
+        st = lib().fc_residual_norm(_ptr(x), _ptr(residual), code, T, H, _ptr(w_post), _ptr(gate),
+                                    gate_tokens, _ptr(w_pre), res_scale, out_scale, eps, _ptr(h),
+                                    _ptr(y), _stream(stream, dev))
+    _check(st, "fc_residual_norm")
+    return h, y
+
+
+def fc_dequantize_residual_norm(codes2, s2, z2, T: int, H: int, bits: int, group2: int,
+                                residual: torch.Tensor, w_post=None, w_pre=None, gate=None,
+                                gate_tokens: int | None = None, eps: float = 1e-5,
+                                res_scale: float = 1.0, out_scale: float = 1.0, h=None, y=None,
+                                stream=None):
+    """fc_residual_norm of the dequantized stage-2 payload (as for fc_dequantize_residual,
+    but not rounded to 16 bits before the norms) -> (h, y)."""
+    for n, t in (("codes2", codes2), ("s2", s2), ("z2", z2), ("residual", residual)):
+        _dev_tensor(t, n)
+    dev = residual.device
+    code, gate_tokens, h, y = _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
+    _room(codes2, "codes2", T * H * bits // 8, dev)
+    meta = T * (H // group2 if group2 > 0 else 0) * 2
+    _room(s2, "s2", meta, dev)
+    _room(z2, "z2", meta, dev)
+    with _on(dev):
+        st = lib().fc_dequantize_residual_norm(_ptr(codes2), _ptr(s2), _ptr(z2), T, H, bits, group2,
+                                               code, _ptr(residual), _ptr(w_post), _ptr(gate),
+                                               gate_tokens, _ptr(w_pre), res_scale, out_scale, eps,
+                                               _ptr(h), _ptr(y), _stream(stream, dev))
+    _check(st, "fc_dequantize_residual_norm")
+    return h, y
+
+
+def fc_allreduce_emulated_norm(x: torch.Tensor, bits: int, group: int, residual: torch.Tensor,
+                               w_post=None, w_pre=None, gate=None, gate_tokens: int | None = None,
+                               eps: float = 1e-5, res_scale: float = 1.0, out_scale: float = 1.0,
+                               h=None, y=None, workspace=None, stream=None, bits2: int | None = None):
+    """x [R, T, H] -> (h, y, workspace): the emulated all-reduce whose last step is
+    fc_dequantize_residual_norm. Payloads as fc_allreduce_emulated leaves them."""
+    _dev_tensor(x, "x")
+    bits2 = bits if bits2 is None else bits2
+    R, T, H = x.shape
+    dev = x.device
+    _like(residual, "residual", (T, H), x.dtype, dev)
+    code, gate_tokens, h, y = _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
+    if workspace is None:
+        workspace = _empty(max(fc_workspace_bytes(R, T, H, bits, group, bits2), 1), torch.uint8, dev, stream)
+    _room(workspace, "workspace", 0, dev)
+    with _on(dev):
+        st = lib().fc_allreduce_emulated_norm(_ptr(x), code, R, T, H, bits, bits2, group, _ptr(residual),
+                                              _ptr(w_post), _ptr(gate), gate_tokens, _ptr(w_pre),
+                                              res_scale, out_scale, eps, _ptr(h), _ptr(y),
+                                              _ptr(workspace),
+                                              workspace.numel() * workspace.element_size(),
+                                              _stream(stream, dev))
+    _check(st, "fc_allreduce_emulated_norm")
+    return h, y, workspace
+
+
+def _mx_padded(K: int) -> int:
+    return -(-K // 128) * 128
+
+
+def _rows3(t: torch.Tensor, name: str):
+    """[R, rows, n] of a 3-D tensor, [1, rows, n] of a 2-D one."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must have 2 or 3 dimensions")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def _mx_operand(codes, scales, name: str, device):
+    """MXFP4 codes [..., rows, Kp/2] with scales [..., rows, Kp/32] -> (R, rows, Kp)."""
+    _dev_tensor(codes, f"{name}codes")
+    R, rows, half = _rows3(codes, f"{name}codes")
+    if half == 0 or half % 64 != 0:
+        raise ValueError(f"{name}codes must hold a positive multiple of 64 bytes a row, not {half}")
+    _like(codes, f"{name}codes", codes.shape, torch.uint8, device)
+    _like(scales, f"{name}scales", (*codes.shape[:-1], half // 16), torch.uint8, device)
+    return R, rows, 2 * half
+
+
+def fc_quantize_mxfp4(x: torch.Tensor, codes=None, scales=None, stream=None):
+    """x [..., K] fp16/bf16 (2 or 3 dimensions) -> MXFP4 (codes [..., Kp/2], scales
+    [..., Kp/32]) uint8, Kp = K rounded up to a multiple of 128 (the padding is zeros)."""
+    _dev_tensor(x, "x")
+    R, T, K = _rows3(x, "x")
+    dev, Kp = x.device, _mx_padded(K)
+    if codes is None:
+        codes = _empty((*x.shape[:-1], Kp // 2), torch.uint8, dev, stream)
+    if scales is None:
+        scales = _empty((*x.shape[:-1], Kp // 32), torch.uint8, dev, stream)
+    _like(codes, "codes", (*x.shape[:-1], Kp // 2), torch.uint8, dev)
+    _like(scales, "scales", (*x.shape[:-1], Kp // 32), torch.uint8, dev)
+    with _on(dev):
+        st = lib().fc_quantize_mxfp4(_ptr(x), _dt(x, "x"), R, T, K, _ptr(codes), _ptr(scales),
+                                     _stream(stream, dev))
+    _check(st, "fc_quantize_mxfp4")
+    return codes, scales
+
+
+def fc_dequantize_mxfp4(codes, scales, K: int, dtype: torch.dtype, out=None, stream=None):
+    """MXFP4 codes [..., Kp/2] and scales [..., Kp/32] -> out [..., K] of `dtype`."""
+    _dev_tensor(codes, "codes")
+    dev = codes.device
+    R, T, Kp = _mx_operand(codes, scales, "", dev)
+    if K < 1 or _mx_padded(K) != Kp:
+        raise ValueError(f"codes hold rows of {Kp} values, K is {K}")
+    if out is None:
+        out = _empty((*codes.shape[:-1], K), dtype, dev, stream)
+    _like(out, "out", (*codes.shape[:-1], K), dtype, dev)
+    with _on(dev):
+        st = lib().fc_dequantize_mxfp4(_ptr(codes), _ptr(scales), R, T, K, _dt(out, "out"), _ptr(out),
+                                       _stream(stream, dev))
+    _check(st, "fc_dequantize_mxfp4")
+    return out
+
+
+def _product_out(y, lead, T, H, dtype, device, stream):
+    if y is None:
+        y = _empty((*lead, T, H), dtype, device, stream)
+    _like(y, "y", (*lead, T, H), dtype, device)
+    return y
+
+
+def fc_matmul_mxfp4(a_codes, a_scales, w_codes, w_scales, dtype: torch.dtype, y=None, stream=None):
+    """MXFP4 a [R, T, K] and w [R, H, K] (or both without R) -> y [R, T, H] = a @ w^T of
+    `dtype`, accumulated in binary32."""
+    _dev_tensor(a_codes, "a_codes")
+    dev = a_codes.device
+    R, T, Kp = _mx_operand(a_codes, a_scales, "a_", dev)
+    Rw, H, Kw = _mx_operand(w_codes, w_scales, "w_", dev)
+    if (R, Kp, a_codes.dim()) != (Rw, Kw, w_codes.dim()):
+        raise ValueError("a must be [R, T, K] and w [R, H, K]")
+    y = _product_out(y, a_codes.shape[:-2], T, H, dtype, dev, stream)
+    with _on(dev):
+        st = lib().fc_matmul_mxfp4(_ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), R, T, Kp,
+                                   H, _dt(y, "y"), _ptr(y), _stream(stream, dev))
+    _check(st, "fc_matmul_mxfp4")
+    return y
+
+
+def fc_linear_mxfp4_workspace_bytes(R: int, T: int, K: int) -> int:
+    return lib().fc_linear_mxfp4_workspace_bytes(R, T, K)
+
+
+def fc_linear_mxfp4(a: torch.Tensor, w_codes, w_scales, y=None, workspace=None, stream=None):
+    """a [R, T, K] fp16/bf16 (quantized to MXFP4 in the call) times MXFP4 weights
+    w [R, H, K] (or both without R) -> y [R, T, H] = a @ w^T of a's dtype."""
+    _dev_tensor(a, "a")
+    R, T, K = _rows3(a, "a")
+    dev = a.device
+    Rw, H, Kw = _mx_operand(w_codes, w_scales, "w_", dev)
+    if (R, _mx_padded(K), a.dim()) != (Rw, Kw, w_codes.dim()):
+        raise ValueError("a must be [R, T, K] and w [R, H, K]")
+    y = _product_out(y, a.shape[:-2], T, H, a.dtype, dev, stream)
+    need = fc_linear_mxfp4_workspace_bytes(R, T, K)
+    if workspace is None and need:
+        workspace = _empty(need, torch.uint8, dev, stream)
+    have = 0
+    if workspace is not None:
+        _room(workspace, "workspace", 0, dev)
+        have = workspace.numel() * workspace.element_size()
+    with _on(dev):
+        st = lib().fc_linear_mxfp4(_ptr(a), _ptr(w_codes), _ptr(w_scales), _dt(a, "a"), R, T, K, H, _ptr(y),
+                                   _ptr(workspace), have, _stream(stream, dev))
+    _check(st, "fc_linear_mxfp4")
+    return y

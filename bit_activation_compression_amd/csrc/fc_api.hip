@@ -7,8 +7,10 @@
 #include <initializer_list>
 
 #include "fc.h"
+#include "fc/layer.h"
 #include "fc_launch.h"
 #include "fc_validate.h"
+#include "fc_validate_layer.h"
 
 namespace {
 
@@ -108,6 +110,34 @@ void *noalloc_scratch() {
         cached[dev].store(p, std::memory_order_release);
     }
     return p;
+}
+
+fc::NormArgs norm_args(int T, int H, const void *residual, const void *w_post, const void *gate,
+                       int gate_tokens, const void *w_pre, float res_scale, float out_scale,
+                       float eps, void *h, void *y) {
+    fc::NormArgs a = {};
+    a.residual = static_cast<const uint16_t *>(residual);
+    a.w_post = static_cast<const uint16_t *>(w_post);
+    a.gate = static_cast<const uint16_t *>(gate);
+    a.w_pre = static_cast<const uint16_t *>(w_pre);
+    a.gate_tokens = gate_tokens;
+    a.res_scale = res_scale;
+    a.out_scale = out_scale;
+    a.eps = eps;
+    a.inv_h = 1.0f / (float)H;
+    a.h = static_cast<uint16_t *>(h);
+    a.y = static_cast<uint16_t *>(y);
+    a.T = T;
+    a.H = H;
+    return a;
+}
+
+hipError_t run_dequantize_norm(fc::NormArgs a, const uint8_t *codes2, const uint16_t *s2,
+                               const uint16_t *z2, int bits, int g2, fc_dtype dt, hipStream_t stream) {
+    a.codes = codes2;
+    a.s = s2;
+    a.z = z2;
+    return fc::launch_dequantize_residual_norm(a, (int)dt, bits, g2, stream);
 }
 
 }  // namespace
@@ -279,6 +309,160 @@ int fc_stage2_group(int R, int H, int group) {
     return g2;
 }
 
+// --- include/fc/layer.h ------------------------------------------------------
+
+fc_status fc_residual_norm(const void *x, const void *residual, fc_dtype dt, int T, int H,
+                           const void *w_post, const void *gate, int gate_tokens,
+                           const void *w_pre, float res_scale, float out_scale, float eps, void *h,
+                           void *y, void *stream) {
+    const size_t n = (size_t)(T > 0 ? T : 0) * (size_t)(H > 0 ? H : 0);
+    const fc_status st = check_norm(T, H, dt, {{x, n * 2}}, residual, w_post, gate, gate_tokens, w_pre,
+                                    res_scale, out_scale, eps, h, y);
+    if (st != FC_OK || T == 0) return st;
+    fc::NormArgs a = norm_args(T, H, residual, w_post, gate, gate_tokens, w_pre, res_scale, out_scale,
+                               eps, h, y);
+    a.x = static_cast<const uint16_t *>(x);
+    return from_hip(fc::launch_residual_norm(a, (int)dt, static_cast<hipStream_t>(stream)));
+}
+
+fc_status fc_dequantize_residual_norm(const uint8_t *codes2, const uint16_t *s2,
+                                      const uint16_t *z2, int T, int H, int bits, int group2,
+                                      fc_dtype dt, const void *residual, const void *w_post,
+                                      const void *gate, int gate_tokens, const void *w_pre,
+                                      float res_scale, float out_scale, float eps, void *h,
+                                      void *y, void *stream) {
+    if (bits != 4 && bits != 8) return FC_ERR_BITS;
+    if (H < 1 || !group_ok(group2) || H % group2 != 0) return FC_ERR_SHAPE;
+    const size_t n = (size_t)(T > 0 ? T : 0) * (size_t)H;
+    const size_t meta = n / (size_t)group2 * 2;
+    const fc_status st = check_norm(T, H, dt, {{codes2, n * (size_t)bits / 8}, {s2, meta}, {z2, meta}},
+                                    residual, w_post, gate, gate_tokens, w_pre, res_scale, out_scale,
+                                    eps, h, y);
+    if (st != FC_OK || T == 0) return st;
+    return from_hip(run_dequantize_norm(norm_args(T, H, residual, w_post, gate, gate_tokens, w_pre,
+                                                  res_scale, out_scale, eps, h, y),
+                                        codes2, s2, z2, bits, group2, dt,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+fc_status fc_allreduce_emulated_norm(const void *x, fc_dtype dt, int R, int T, int H, int bits1,
+                                     int bits2, int group, const void *residual,
+                                     const void *w_post, const void *gate, int gate_tokens,
+                                     const void *w_pre, float res_scale, float out_scale,
+                                     float eps, void *h, void *y, void *workspace,
+                                     size_t workspace_bytes, void *stream) {
+    int g2 = 0;
+    fc_status st = check_shape2(R, T, H, bits1, bits2, group, &g2);
+    if (st != FC_OK) return st;
+    const Layout L = layout(R, T, H, bits1, bits2, group, g2);
+    const uint64_t n = (uint64_t)T * (uint64_t)H;
+    st = check_norm(T, H, dt, {{x, n * (uint64_t)R * 2}, {workspace, L.total}}, residual, w_post, gate,
+                    gate_tokens, w_pre, res_scale, out_scale, eps, h, y);
+    if (st != FC_OK) return st;
+    if (n == 0) return FC_OK;
+    if (workspace_bytes < L.total) return FC_ERR_WORKSPACE;
+    // the workspace is written: no input may lie in it
+    const Span ws = {workspace, L.total};
+    const size_t row = (size_t)H * 2;
+    const size_t gates = gate ? ((size_t)T + (size_t)gate_tokens - 1) / (size_t)gate_tokens : 0;
+    st = check_overlap({ws}, {{x, n * (uint64_t)R * 2}, {residual, n * 2}, {w_post, row}, {w_pre, row},
+                              {gate, gates * row}});
+    if (st != FC_OK) return st;
+    uint8_t *wb = static_cast<uint8_t *>(workspace);
+    uint16_t *s1 = reinterpret_cast<uint16_t *>(wb + L.off[1]);
+    uint16_t *z1 = reinterpret_cast<uint16_t *>(wb + L.off[2]);
+    uint8_t *codes2 = wb + L.off[3];
+    uint16_t *s2 = reinterpret_cast<uint16_t *>(wb + L.off[4]);
+    uint16_t *z2 = reinterpret_cast<uint16_t *>(wb + L.off[5]);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = from_hip(run_quantize(x, dt, n * (uint64_t)R, bits1, group, wb, s1, z1, s));
+    if (st != FC_OK) return st;
+    st = from_hip(run_dsr(wb, s1, z1, R, n, bits1, bits2, group, g2, codes2, s2, z2, s));
+    if (st != FC_OK) return st;
+    return from_hip(run_dequantize_norm(norm_args(T, H, residual, w_post, gate, gate_tokens, w_pre,
+                                                  res_scale, out_scale, eps, h, y),
+                                        codes2, s2, z2, bits2, g2, dt, s));
+}
+
+fc_status fc_quantize_mxfp4(const void *x, fc_dtype dt, int R, int T, int K, uint8_t *codes,
+                            uint8_t *scales, void *stream) {
+    fc_status st = check_mx(R, T, K);
+    if (st != FC_OK) return st;
+    if (dt != FC_F16 && dt != FC_BF16) return FC_ERR_DTYPE;
+    const uint64_t rows = (uint64_t)R * (uint64_t)T;
+    st = check_ptrs(rows, {x, codes, scales});
+    if (st != FC_OK || rows == 0) return st;
+    st = check_overlap({{codes, mx_code_bytes(R, T, K)}, {scales, mx_scale_bytes(R, T, K)}},
+                       {{x, rows * (uint64_t)K * 2}});
+    if (st != FC_OK) return st;
+    return from_hip(fc::launch_quantize_mxfp4(static_cast<const uint16_t *>(x), (int)dt, rows, K,
+                                              (int)mx_padded(K), codes, scales,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+fc_status fc_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int R, int T, int K,
+                              fc_dtype dt, void *out, void *stream) {
+    fc_status st = check_mx(R, T, K);
+    if (st != FC_OK) return st;
+    if (dt != FC_F16 && dt != FC_BF16) return FC_ERR_DTYPE;
+    const uint64_t rows = (uint64_t)R * (uint64_t)T;
+    st = check_ptrs(rows, {codes, scales, out});
+    if (st != FC_OK || rows == 0) return st;
+    st = check_overlap({{out, rows * (uint64_t)K * 2}},
+                       {{codes, mx_code_bytes(R, T, K)}, {scales, mx_scale_bytes(R, T, K)}});
+    if (st != FC_OK) return st;
+    return from_hip(fc::launch_dequantize_mxfp4(codes, scales, rows, K, (int)mx_padded(K), (int)dt,
+                                                static_cast<uint16_t *>(out),
+                                                static_cast<hipStream_t>(stream)));
+}
+
+fc_status fc_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,
+                          const uint8_t *w_scales, int R, int T, int K, int H, fc_dtype dt,
+                          void *y, void *stream) {
+    fc_status st = check_mx_product(R, T, K, H);
+    if (st != FC_OK) return st;
+    if (dt != FC_F16 && dt != FC_BF16) return FC_ERR_DTYPE;
+    st = check_ptrs((size_t)T, {a_codes, a_scales, w_codes, w_scales, y});
+    if (st != FC_OK || T == 0) return st;
+    st = check_overlap({{y, (size_t)R * (size_t)T * (size_t)H * 2}},
+                       {{a_codes, mx_code_bytes(R, T, K)}, {a_scales, mx_scale_bytes(R, T, K)},
+                        {w_codes, mx_code_bytes(R, H, K)}, {w_scales, mx_scale_bytes(R, H, K)}});
+    if (st != FC_OK) return st;
+    return from_hip(fc::launch_matmul_mxfp4(a_codes, a_scales, w_codes, w_scales, R, T,
+                                            (int)mx_padded(K), H, (int)dt, static_cast<uint16_t *>(y),
+                                            static_cast<hipStream_t>(stream)));
+}
+
+fc_status fc_linear_mxfp4(const void *a, const uint8_t *w_codes, const uint8_t *w_scales,
+                          fc_dtype dt, int R, int T, int K, int H, void *y, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    fc_status st = check_mx_product(R, T, K, H);
+    if (st != FC_OK) return st;
+    if (dt != FC_F16 && dt != FC_BF16) return FC_ERR_DTYPE;
+    st = check_ptrs((size_t)T, {a, w_codes, w_scales, y, workspace});
+    if (st != FC_OK || T == 0) return st;
+    const size_t need = fc_linear_mxfp4_workspace_bytes(R, T, K);
+    if (workspace_bytes < need) return FC_ERR_WORKSPACE;
+    st = check_overlap({{y, (size_t)R * (size_t)T * (size_t)H * 2}, {workspace, need}},
+                       {{a, (size_t)R * (size_t)T * (size_t)K * 2},
+                        {w_codes, mx_code_bytes(R, H, K)}, {w_scales, mx_scale_bytes(R, H, K)}});
+    if (st != FC_OK) return st;
+    const int Kp = (int)mx_padded(K);
+    uint8_t *codes = static_cast<uint8_t *>(workspace);
+    uint8_t *scales = codes + mx_workspace_scales(R, T, K);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    st = from_hip(fc::launch_quantize_mxfp4(static_cast<const uint16_t *>(a), (int)dt,
+                                            (uint64_t)R * (uint64_t)T, K, Kp, codes, scales, s));
+    if (st != FC_OK) return st;
+    return from_hip(fc::launch_matmul_mxfp4(codes, scales, w_codes, w_scales, R, T, Kp, H, (int)dt,
+                                            static_cast<uint16_t *>(y), s));
+}
+
+size_t fc_linear_mxfp4_workspace_bytes(int R, int T, int K) {
+    if (check_mx(R, T, K) != FC_OK || T == 0) return 0;
+    return mx_workspace_scales(R, T, K) + mx_scale_bytes(R, T, K);
+}
+
 const char *fc_status_string(fc_status s) {
     switch (s) {
     case FC_OK: return "FC_OK";
@@ -291,6 +475,8 @@ const char *fc_status_string(fc_status s) {
     case FC_ERR_DTYPE: return "FC_ERR_DTYPE: dtype must be FC_F16 or FC_BF16";
     case FC_ERR_SCRATCH:
         return "FC_ERR_SCRATCH: the payloads exceed the library's scratch (FC_NOALLOC_SCRATCH_BYTES)";
+    case FC_ERR_OVERLAP: return "FC_ERR_OVERLAP: an output overlaps another buffer";
+    case FC_ERR_VALUE: return "FC_ERR_VALUE: a scale or eps is outside its range";
     }
     return "unknown fc_status";
 }

@@ -67,4 +67,35 @@ hipError_t launch_dequantize_generic(const uint8_t *codes2, const uint16_t *s2, 
 hipError_t launch_sum(const uint16_t *x, int dtype, int R, uint64_t n, uint16_t *out,
                       hipStream_t stream);
 
+// Block norms (include/fc/layer.h) of T rows of H: x (a 16-bit block output)
+// or codes, s, z (a payload; groups, gmagic: set by its launcher). w_post, gate
+// and w_pre (with y) may be NULL; h may be residual.
+struct NormArgs {
+    const uint16_t *x;
+    const uint8_t *codes;
+    const uint16_t *s, *z;
+    int groups;           // groups of a row
+    uint32_t gmagic;      // reciprocal of the group length, see fc_norm.h
+    const uint16_t *residual, *w_post, *gate, *w_pre;
+    int gate_tokens;
+    float res_scale, out_scale, eps, inv_h;
+    uint16_t *h, *y;
+    int T, H;
+};
+hipError_t launch_residual_norm(const NormArgs &a, int dtype, hipStream_t stream);
+hipError_t launch_dequantize_residual_norm(const NormArgs &a, int dtype, int bits, int group,
+                                           hipStream_t stream);
+
+// MXFP4 codes and scales of `rows` rows of K 16-bit values, padded to Kp (a
+// multiple of 128): codes [rows][Kp/2], scales [rows][Kp/32]; and back.
+hipError_t launch_quantize_mxfp4(const uint16_t *x, int dtype, uint64_t rows, int K, int Kp,
+                                 uint8_t *codes, uint8_t *scales, hipStream_t stream);
+hipError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, uint64_t rows, int K,
+                                   int Kp, int dtype, uint16_t *out, hipStream_t stream);
+
+// y[r] = a[r] w[r]^T of MXFP4 operands: a [R][T][Kp], w [R][H][Kp], y [R][T][H].
+hipError_t launch_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
+                               const uint8_t *w_codes, const uint8_t *w_scales, int R, int T, int Kp,
+                               int H, int dtype, uint16_t *y, hipStream_t stream);
+
 }  // namespace fc

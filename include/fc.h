@@ -70,7 +70,9 @@ typedef enum {
     FC_ERR_WORKSPACE = 5,  /* workspace smaller than fc_workspace_bytes() */
     FC_ERR_LAUNCH = 6,     /* the HIP runtime reported an error at launch */
     FC_ERR_DTYPE = 7,      /* dtype is not FC_F16 or FC_BF16 */
-    FC_ERR_SCRATCH = 8     /* the payloads exceed FC_NOALLOC_SCRATCH_BYTES */
+    FC_ERR_SCRATCH = 8,    /* the payloads exceed FC_NOALLOC_SCRATCH_BYTES */
+    FC_ERR_OVERLAP = 9,    /* an output overlaps another buffer (fc/layer.h) */
+    FC_ERR_VALUE = 10      /* a scale or eps outside its range (fc/layer.h) */
 } fc_status;
 
 typedef enum { FC_F16 = 0, FC_BF16 = 1 } fc_dtype;

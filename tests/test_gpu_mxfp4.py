@@ -1,0 +1,344 @@
+"""MXFP4 on the GPU against the 64-bit statements (tests/layer_ref.py): the
+quantizer and the dequantizer bit for bit over every 16-bit value and every
+code and scale, the product bit for bit on operands whose sums binary32 holds
+exactly and within the accumulation bound on others, and the three together
+with the all-reduce as a transformer block runs them."""
+from __future__ import annotations
+
+import sys
+
+import pytest
+import torch
+
+import bit_activation_compression_amd as fc
+import layer_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a ROCm GPU")
+    fc.lib()
+    yield
+
+
+def _say(msg):
+    print(f"[gpu] {msg}", file=sys.stderr, flush=True)
+
+
+def _guarded(shape, dtype):
+    n = 1
+    for s in shape:
+        n *= s
+    size = torch.empty(0, dtype=dtype).element_size()
+    raw = torch.full((512 + n * size + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    def check():
+        assert (raw[:512] == 0x5A).all() and (raw[512 + n * size:] == 0x5A).all()
+    return raw[512:512 + n * size].view(dtype).view(shape), check
+
+
+def _quantize(x):
+    """GPU codes and scales of a CPU tensor, with the bytes around them checked."""
+    Kp = -(-x.shape[-1] // 128) * 128
+    codes, c1 = _guarded((*x.shape[:-1], Kp // 2), torch.uint8)
+    scales, c2 = _guarded((*x.shape[:-1], Kp // 32), torch.uint8)
+    fc.fc_quantize_mxfp4(x.cuda(), codes, scales)
+    torch.cuda.synchronize()
+    c1(), c2()
+    return codes, scales
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_quantize_every_value(dt):
+    """Every finite bit pattern, in blocks of neighbours (as neighbouring magnitudes) and in blocks
+    whose scale another value sets."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(dt)
+    bits = bits[torch.isfinite(bits.float())]
+    bits = torch.cat((bits, torch.zeros(-len(bits) % 32, dtype=dt)))
+    rows = [bits]
+    for top in ([1.0, 1.75, 2.0 ** -10, 2.0 ** 15 - 16, 2.0 ** -24] if dt == F16
+                else [1.0, 1.75, 2.0 ** 120, 2.0 ** 127, 2.0 ** -100, 2.0 ** -124, 2.0 ** -126, 2.0 ** -133]):
+        small = bits[bits.float().abs() <= top]
+        small = torch.cat((small, torch.zeros(-len(small) % 31, dtype=dt))).view(-1, 31)
+        b = torch.cat((small, torch.full((len(small), 1), top, dtype=dt)), 1).flatten()
+        rows.append(torch.cat((b, torch.zeros(-len(b) % 128, dtype=dt))))
+    for i, x in enumerate(rows):
+        _say(f"quantize every value {dt} set {i}")
+        codes, scales = _quantize(x[None])
+        want = ref.mx_quantize(x[None].double())
+        assert torch.equal(scales.cpu(), want[1])
+        assert torch.equal(codes.cpu(), want[0])
+
+
+SHAPES = [(1, 1), (3, 31), (2, 32), (5, 33), (4, 100), (7, 127), (1, 128), (9, 129), (2, 250), (130, 256), (3, 4100),
+          (65, 4096), (1000, 200), (2, 5, 96), (4, 33, 640), (1, 70001), (3, 65536)]
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_quantize_shapes_and_back(shape, dt):
+    _say(f"quantize {shape} {dt}")
+    g = torch.Generator().manual_seed(sum(shape))
+    x = (torch.randn(shape, generator=g) * torch.exp2(torch.randint(-8, 8, shape, generator=g).float())).to(dt)
+    x[..., ::7] = 0
+    codes, scales = _quantize(x)
+    want = ref.mx_quantize(x.double())
+    assert torch.equal(codes.cpu(), want[0]) and torch.equal(scales.cpu(), want[1])
+    out, check = _guarded(shape, dt)
+    fc.fc_dequantize_mxfp4(codes, scales, shape[-1], dt, out)
+    torch.cuda.synchronize()
+    check()
+    assert torch.equal(out.cpu(), ref.mx_dequantize(*want, shape[-1]).to(dt))
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_non_finite_blocks(dt):
+    x = torch.randn((4, 160), generator=torch.Generator().manual_seed(1)).to(dt)
+    x[0, 5] = float("nan")
+    x[1, 40] = float("inf")
+    x[2, 159] = -float("inf")
+    codes, scales = _quantize(x)
+    want = ref.mx_quantize(x.double())
+    assert torch.equal(codes.cpu(), want[0]) and torch.equal(scales.cpu(), want[1])
+    out = fc.fc_dequantize_mxfp4(codes, scales, 160, dt).cpu()
+    bad = torch.zeros(4, 160, dtype=torch.bool)
+    bad[0, :32], bad[1, 32:64], bad[2, 128:] = True, True, True
+    assert torch.equal(torch.isnan(out), bad)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_dequantize_every_code_and_scale(dt):
+    """256 code pairs x 256 scales: exact, or rounded once, infinite past the type's range, NaN for 255."""
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8)[None].repeat(256, 1)       # 512 values a row
+    scales = torch.arange(256, dtype=torch.int32).to(torch.uint8)[:, None].repeat(1, 16)
+    out = fc.fc_dequantize_mxfp4(codes.cuda(), scales.cuda(), 512, dt).cpu()
+    want = ref.mx_dequantize(codes, scales, 512).to(dt)     # at most 2 significant bits: one rounding
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    ok = ~torch.isnan(want)
+    assert torch.equal(out[ok].view(torch.int16), want[ok].view(torch.int16))
+
+
+# (R, T, K, H): single tokens, borders of every token and channel tile, odd sizes, short and long rows
+PRODUCTS = [(1, 1, 128, 16), (1, 1, 32, 1), (2, 1, 2048, 512), (1, 2, 100, 7), (3, 5, 384, 33), (1, 8, 4096, 64),
+            (4, 13, 640, 130), (1, 15, 256, 65), (2, 16, 1152, 256), (1, 17, 256, 300), (1, 31, 512, 128), (2, 32, 3584, 48),
+            (1, 33, 896, 257), (2, 63, 384, 96), (1, 64, 7168, 160), (1, 65, 256, 64), (3, 77, 640, 515), (1, 100, 2176, 1000),
+            (1, 127, 1000, 120), (2, 128, 512, 128), (1, 129, 384, 255), (1, 200, 4224, 264), (2, 255, 256, 256),
+            (1, 256, 1024, 512), (1, 257, 896, 700), (2, 300, 128, 768), (1, 512, 2048, 1024), (1, 1000, 640, 1000),
+            (4, 520, 256, 300), (1, 2048, 256, 2048), (2, 1030, 1152, 1300), (1, 4000, 128, 40), (1, 40, 128, 4000),
+            (8, 3, 256, 2050), (1, 700, 96, 5)]
+
+
+def _operands(R, T, K, H, seed, spread):
+    g = torch.Generator().manual_seed(seed)
+    Kp = -(-K // 128) * 128
+    def side(rows):
+        codes = torch.randint(0, 256, (R, rows, Kp // 2), generator=g, dtype=torch.uint8)
+        codes[..., (K + 1) // 2:] = 0
+        if K % 2:
+            codes[..., K // 2] &= 15
+        scales = torch.randint(127 - spread, 128 + spread, (R, rows, Kp // 32), generator=g).to(torch.uint8)
+        scales[..., -(-K // 32):] = 0
+        return codes, scales
+    return *side(T), *side(H)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("R,T,K,H", PRODUCTS)
+def test_product_exact(R, T, K, H, dt):
+    """Scales of 1: every product is a multiple of 1/4 and every partial sum below 2^24 of them
+    (K * 36 * 4 < 2^24), so binary32 holds the sum exactly in any order."""
+    _say(f"product exact R={R} T={T} K={K} H={H} {dt}")
+    assert K * 36 * 4 < 2 ** 24
+    ac, as_, wc, ws = _operands(R, T, K, H, T + K + H, 0)
+    y, check = _guarded((R, T, H), dt)
+    fc.fc_matmul_mxfp4(ac.cuda(), as_.cuda(), wc.cuda(), ws.cuda(), dt, y)
+    torch.cuda.synchronize()
+    check()
+    want, _ = ref.mx_product(ref.mx_dequantize(ac, as_, K), ref.mx_dequantize(wc, ws, K))
+    assert torch.equal(y.cpu(), want.to(torch.float32).to(dt))
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("R,T,K,H", PRODUCTS)
+def test_product_scales(R, T, K, H, dt):
+    """Scales of 2^-3 to 2^3, each its own: K additions of 2^-24 of the magnitudes' sum, and twice
+    that for a matrix core that truncates where it aligns its terms."""
+    _say(f"product scales R={R} T={T} K={K} H={H} {dt}")
+    ac, as_, wc, ws = _operands(R, T, K, H, 3 * T + K + H, 3)
+    y = fc.fc_matmul_mxfp4(ac.cuda(), as_.cuda(), wc.cuda(), ws.cuda(), dt)
+    torch.cuda.synchronize()
+    want, mag = ref.mx_product(ref.mx_dequantize(ac, as_, K), ref.mx_dequantize(wc, ws, K))
+    if dt == F16:
+        assert want.abs().max() < 65504
+    ref.assert_within(y, want, dt, mag * (K * 2.0 ** -23))
+    again = fc.fc_matmul_mxfp4(ac.cuda(), as_.cuda(), wc.cuda(), ws.cuda(), dt)
+    assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("R,T,K,H", PRODUCTS)
+def test_linear_quantizes_its_activations(R, T, K, H, dt):
+    """fc_linear_mxfp4 of integer activations: the product of fc_quantize_mxfp4's codes, exactly."""
+    _say(f"linear R={R} T={T} K={K} H={H} {dt}")
+    _, _, wc, ws = _operands(R, 1, K, H, K + H, 0)
+    g = torch.Generator().manual_seed(T)
+    # magnitudes 0..12 and a 4 in every block: scales of 1 or 2, codes rounded and saturated
+    a = torch.randint(-12, 13, (R, T, K), generator=g).to(dt)
+    a[..., ::32] = 4
+    y, check = _guarded((R, T, H), dt)
+    fc.fc_linear_mxfp4(a.cuda(), wc.cuda(), ws.cuda(), y)
+    torch.cuda.synchronize()
+    check()
+    ac, as_ = ref.mx_quantize(a.double())
+    want, _ = ref.mx_product(ref.mx_dequantize(ac, as_, K), ref.mx_dequantize(wc, ws, K))
+    assert K * 72 * 4 < 2 ** 24
+    assert torch.equal(y.cpu(), want.to(torch.float32).to(dt))
+
+
+@pytest.mark.parametrize("T", [1, 16, 40, 300])
+def test_linear_real_activations(T):
+    R, K, H = 2, 1000, 200
+    g = torch.Generator().manual_seed(T)
+    a = torch.randn((R, T, K), generator=g).to(BF16)
+    a[:, :, 3] *= 50
+    a[0, 0] = 0
+    w = torch.randn((R, H, K), generator=g).to(BF16)
+    wc, ws = fc.fc_quantize_mxfp4(w.cuda())
+    y = fc.fc_linear_mxfp4(a.cuda(), wc, ws)
+    q = fc.fc_quantize_mxfp4(a.cuda())
+    want, mag = ref.mx_product(ref.mx_dequantize(*(v.cpu() for v in q), K), ref.mx_dequantize(wc.cpu(), ws.cpu(), K))
+    ref.assert_within(y, want, BF16, mag * (K * 2.0 ** -23))
+    assert (y[0, 0] == 0).all()
+
+
+@pytest.mark.parametrize("T,H", [(1, 64), (16, 96), (50, 64), (300, 512)])
+def test_nan_scales_stay_in_their_row_and_channel(T, H):
+    K = 512
+    g = torch.Generator().manual_seed(T)
+    a = torch.randn((1, T, K), generator=g).to(BF16)
+    a[0, T // 2, 400] = float("nan")
+    ac, as_, wc, ws = _operands(1, T, K, H, 1, 1)
+    ws[0, 7, 3] = 255
+    bad = torch.zeros(1, T, H, dtype=torch.bool)
+    bad[:, T // 2], bad[..., 7] = True, True
+    y = fc.fc_linear_mxfp4(a.cuda(), wc.cuda(), ws.cuda())
+    assert torch.equal(torch.isnan(y.cpu()), bad)
+    y = fc.fc_matmul_mxfp4(*fc.fc_quantize_mxfp4(a.cuda()), wc.cuda(), ws.cuda(), BF16)
+    assert torch.equal(torch.isnan(y.cpu()), bad)
+
+
+@pytest.mark.parametrize("T", [1, 20, 300])
+def test_extreme_scales(T):
+    """Products of 2^-127 and 2^120 scales: neither side alone fits a product in range."""
+    K, H = 256, 48
+    ac, as_, wc, ws = _operands(1, T, K, H, T, 0)
+    as_[..., :] = 0
+    ws[..., :] = 247
+    y = fc.fc_matmul_mxfp4(ac.cuda(), as_.cuda(), wc.cuda(), ws.cuda(), BF16)
+    want, _ = ref.mx_product(ref.mx_dequantize(ac, as_, K), ref.mx_dequantize(wc, ws, K))
+    assert torch.equal(y.cpu(), want.to(torch.float32).to(BF16))
+
+
+def test_two_dimensional_operands_and_no_tokens():
+    ac, as_, wc, ws = (v.cuda() for v in _operands(1, 5, 256, 40, 2, 1))
+    y = fc.fc_matmul_mxfp4(ac, as_, wc, ws, BF16)
+    y2 = fc.fc_matmul_mxfp4(ac[0], as_[0], wc[0], ws[0], BF16)
+    assert y2.shape == (5, 40) and torch.equal(y[0], y2)
+    empty = fc.fc_linear_mxfp4(torch.empty((2, 0, 256), dtype=BF16, device="cuda"), wc.repeat(2, 1, 1), ws.repeat(2, 1, 1))
+    assert empty.shape == (2, 0, 40)
+    c, s = fc.fc_quantize_mxfp4(torch.empty((0, 100), dtype=F16, device="cuda"))
+    assert c.shape == (0, 64) and s.shape == (0, 4)
+
+
+def test_binding_refuses():
+    x = torch.randn((4, 256), device="cuda").to(BF16)
+    codes, scales = fc.fc_quantize_mxfp4(x)
+    for call in [
+        lambda: fc.fc_quantize_mxfp4(x.float()), lambda: fc.fc_quantize_mxfp4(x[0]), lambda: fc.fc_quantize_mxfp4(x[:, ::2]),
+        lambda: fc.fc_quantize_mxfp4(x.cpu()), lambda: fc.fc_quantize_mxfp4(x, codes=codes[:3]),
+        lambda: fc.fc_quantize_mxfp4(x, scales=scales.to(torch.int8)),
+        lambda: fc.fc_dequantize_mxfp4(codes, scales, 100, BF16), lambda: fc.fc_dequantize_mxfp4(codes, scales[:3], 256, BF16),
+        lambda: fc.fc_dequantize_mxfp4(codes, scales, 256, torch.float32),
+        lambda: fc.fc_matmul_mxfp4(codes, scales, codes[None], scales[None], BF16),
+        lambda: fc.fc_matmul_mxfp4(codes, scales, codes[:, :64].contiguous(), scales[:, :4].contiguous(), BF16),
+        lambda: fc.fc_matmul_mxfp4(codes, scales, codes, scales, BF16, y=torch.empty((4, 5), dtype=BF16, device="cuda")),
+        lambda: fc.fc_linear_mxfp4(x.float(), codes, scales), lambda: fc.fc_linear_mxfp4(x[:, :64].contiguous(), codes, scales),
+        lambda: fc.fc_linear_mxfp4(x, codes, scales, y=torch.empty((4, 4), dtype=F16, device="cuda")),
+    ]:
+        with pytest.raises(ValueError):
+            call()
+    a = torch.randn((300, 256), device="cuda").to(BF16)
+    with pytest.raises(fc.FcError) as e:
+        fc.fc_linear_mxfp4(a, codes, scales, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 5
+    ws = torch.empty(fc.fc_linear_mxfp4_workspace_bytes(1, 300, 256) + 4096, dtype=torch.uint8, device="cuda")
+    with pytest.raises(fc.FcError) as e:
+        fc.fc_linear_mxfp4(a, codes, scales, y=ws[:2400].view(BF16).view(300, 4), workspace=ws)
+    assert e.value.status == 9
+
+
+def test_other_stream_and_graph_replays():
+    R, K, H = 2, 1024, 512
+    for T in (4, 300):
+        a = torch.randn((R, T, K), device="cuda").to(BF16)
+        wc, ws = fc.fc_quantize_mxfp4(torch.randn((R, H, K), device="cuda").to(BF16))
+        y = fc.fc_linear_mxfp4(a, wc, ws)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        y2 = fc.fc_linear_mxfp4(a, wc, ws, stream=side)
+        side.synchronize()
+        assert torch.equal(y, y2)
+        need = max(fc.fc_linear_mxfp4_workspace_bytes(R, T, K), 1)
+        work = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            fc.fc_linear_mxfp4(a, wc, ws, y2, work[0], stream=side)
+        torch.cuda.synchronize()
+        for i in range(4):
+            a.copy_(torch.randn((R, T, K), device="cuda"))
+            y2.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            fc.fc_linear_mxfp4(a, wc, ws, y, work[1])     # beside the replay, with a workspace of its own
+            torch.cuda.synchronize()
+            assert torch.equal(y, y2), f"T={T} replay {i}"
+
+
+def test_block_chain():
+    """The end of a transformer block under tensor parallelism: every rank's MXFP4 projection of its
+    slice, the low-bit all-reduce of the partial sums, the residual update and both norms, and the
+    next projection -- each step against its 64-bit statement on the step's own input."""
+    R, T, K, H, bits, group = 4, 40, 512, 1024, 4, 128
+    g = torch.Generator().manual_seed(11)
+    a = torch.randn((R, T, K), generator=g).to(BF16)
+    w = [torch.randn(s, generator=g).mul(s[-1] ** -0.5).to(BF16).cuda() for s in ((R, H, K), (K, H))]
+    (wc, ws), (vc, vs) = (fc.fc_quantize_mxfp4(v) for v in w)
+    residual = torch.randn((T, H), generator=g).to(BF16)
+    ones = torch.ones(H, dtype=BF16)
+    y = fc.fc_linear_mxfp4(a.cuda(), wc, ws)
+    stream = residual.cuda()
+    h, n, work = fc.fc_allreduce_emulated_norm(y, bits, group, stream, w_post=ones.cuda(), w_pre=ones.cuda(),
+                                               gate=0.5 * ones.cuda(), h=stream)
+    out = fc.fc_linear_mxfp4(n, vc, vs)
+    torch.cuda.synchronize()
+    want, mag = ref.mx_product(ref.mx_dequantize(*ref.mx_quantize(a.double()), K), ref.mx_dequantize(wc.cpu(), ws.cpu(), K))
+    ref.assert_within(y, want, BF16, mag * (K * 2.0 ** -23), "projection")
+    p = fc.workspace_views(work, R, T, H, bits, group)
+    x = ref.dequantize(p["codes2"].cpu(), p["s2"].cpu(), p["z2"].cpu(), bits, group)
+    # the reduced sum is within the two quantizations' steps of the sum of y
+    s1 = p["s1"].cpu().view(torch.float16).double().repeat_interleave(group, -1).sum(0)
+    s2 = p["s2"].cpu().view(torch.float16).double().repeat_interleave(group, -1)
+    total = y.cpu().double().sum(0)
+    assert ((x - total).abs() <= (s1 + s2) / 2 + 2.0 ** -10 * (total.abs() + y.cpu().double().abs().sum(0))).all()
+    d = ones.double()
+    hr, eh, nr, en = ref.norms(x, residual.double(), d, 0.5 * d, T, d, 1.0, 1.0, 1e-5)
+    ref.assert_within(h, hr, BF16, eh, "h")
+    ref.assert_within(n, nr, BF16, en, "n")
+    q = ref.mx_quantize(n.cpu().double())
+    want, mag = ref.mx_product(ref.mx_dequantize(*q, H)[None], ref.mx_dequantize(vc.cpu(), vs.cpu(), H)[None])
+    ref.assert_within(out, want[0], BF16, mag[0] * (H * 2.0 ** -23), "next projection")
