@@ -1,68 +1,399 @@
 // Linear layer on MXFP4 operands (include/fc/layer.h): y[r] = a[r] w[r]^T on
-// the scaled matrix cores, v_mfma_scale_f32_16x16x128_f8f6f4 with both
-// operands FP4: lane l holds row l % 16 of its operand at k = 32 (l / 16) +
-// 0..31, 16 bytes of codes and one scale byte, which is one block of the format.
+// the scaled matrix cores, v_mfma_scale_f32_32x32x64_f8f6f4 with both operands
+// FP4. Lane l holds row l % 32 of its operand at k = 32 (l / 32) + 0..31: 16
+// bytes of codes and one scale byte, which is one block of the format. The row
+// operand is w (channels), the column operand a (tokens): an accumulator holds
+// channels 8 (v / 4) + 4 (l / 32) + v % 4 of token l % 32.
 //
-// The row operand is w (16 channels) and the column operand a (16 tokens), so
-// a lane's four accumulators are 4 consecutive channels of one token.
+// Work layout:
+//   - a workgroup owns a BH (channels) x BT (tokens) tile of one rank's
+//     output, its WH x WT waves (BH / WH) x (BT / WT) each, in 32 x 32 blocks;
+//   - K is walked in stages of 256 (128 bytes of codes and 8 of scales a row,
+//     whole L2 lines), NB of them in LDS, filled straight from global memory
+//     (buffer_load ... lds) NB - 1 stages ahead. The eight 16-byte chunks of a
+//     row are rotated by (row / 2) % 8, so that a fragment read (32 rows x one
+//     chunk) is free of bank conflicts;
+//   - a stage is 4 matrix-core steps of k = 64. Step ks takes blocks 2 ks (lanes
+//     0..31) and 2 ks + 1 (lanes 32..63) of each row: the scale bytes of a row
+//     are read as two words, shifted right by a byte in the upper lanes, and
+//     the instruction's byte selection picks byte 0 or 2;
+//   - rows past H or T, and the second half of the last stage where K is an odd
+//     multiple of 128, lie past the buffer resources and read as zeros;
+//   - workgroups are persistent: stages of consecutive tiles form one stream,
+//     so the next tile's first stages are in flight during a tile's epilogue.
+//     The tiles are split into one contiguous run per XCD (workgroup b runs on
+//     XCD b % 8), in groups of 4 token tiles x all channel tiles, so that the
+//     workgroups of an XCD share operands in its L2.
+#include <atomic>
+
 #include "fc_launch.h"
 #include "fc_mxfp4.h"
 
 namespace fc {
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kFp4 = 4;   // operand format of the f8f6f4 instructions
+constexpr int kFp4 = 4;                   // operand format of the f8f6f4 instructions
+constexpr int kStageBytes = 128;          // bytes of codes of a row in a stage
+constexpr int kStageScales = 8;           // bytes of scales
+constexpr int kStageK = 2 * kStageBytes;
+constexpr int kGroupT = 4;                // token tiles per scheduling group
+constexpr int kXcds = 8;
+constexpr uint32_t kPast = 0xFFFFFFF0u;   // an offset past every resource
+// buffer resource word 3 for raw (untyped, unswizzled) 32-bit-addressed
+// buffers on gfx9-family GPUs
+constexpr int kRawBufferFlags = 0x00020000;
 
-__device__ __forceinline__ i32x8 operand(const u32x4 &v) {
-    return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+// SEL: byte of both scale words (0 or 2)
+template <int SEL>
+__device__ __forceinline__ f32x16 mfma_mx(const u32x4 &w, const u32x4 &a, const f32x16 &c, uint32_t sw,
+                                          uint32_t sa) {
+    const i32x8 wv = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+    const i32x8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, av, c, kFp4, kFp4, SEL, (int)sw, SEL, (int)sa);
 }
 
-__device__ __forceinline__ f32x4 mfma_mx(const u32x4 &w, const u32x4 &a, const f32x4 &c, uint32_t sw,
-                                         uint32_t sa) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a), c, kFp4, kFp4, 0,
-                                                            (int)sw, 0, (int)sa);
+// s_waitcnt until at most N vector-memory operations of this wave are
+// outstanding and all of its LDS operations are done (gfx9 encoding: vmcnt in
+// bits 3:0 and 15:14, expcnt left at its maximum, lgkmcnt 0).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
+// Workgroup barrier that leaves this wave's loads in flight.
+__device__ __forceinline__ void barrier_keep_loads() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 template <int DT>
-__device__ __forceinline__ uint16_t round1(float v) {
-    if constexpr (DT == 1) return __builtin_bit_cast(uint16_t, (__bf16)as_f32(v));
-    else return __builtin_bit_cast(uint16_t, (_Float16)as_f32(v));
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+    const f32x2 pair = {as_f32(a), as_f32(b)};
+    if constexpr (DT == 1) return __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, bf16x2));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, f16x2));
 }
 
-template <int DT>
-__global__ __launch_bounds__(kBlockThreads) void matmul_mxfp4_kernel(
-    const uint8_t *__restrict__ ac, const uint8_t *__restrict__ as, const uint8_t *__restrict__ wc,
-    const uint8_t *__restrict__ ws, int T, int Kp, int H, int tiles_t, int tiles_h,
-    uint64_t tiles, uint16_t *__restrict__ y) {
-    const int lane = lane_id();
-    const uint64_t tile = wave_index();
-    if (tile >= tiles) return;
-    const uint32_t per_rank = (uint32_t)tiles_t * (uint32_t)tiles_h;
-    const uint32_t r = (uint32_t)(tile / per_rank);
-    const uint32_t i = (uint32_t)(tile - (uint64_t)r * per_rank);
-    const int h0 = (int)(i / (uint32_t)tiles_t) * 16, t0 = (int)(i % (uint32_t)tiles_t) * 16;
-    const int row = lane & 15, kb = lane >> 4;
-    const int hr = h0 + row < H ? h0 + row : H - 1;
-    const int tr = t0 + row < T ? t0 + row : T - 1;
-    const uint64_t wrow = (uint64_t)r * (uint32_t)H + (uint32_t)hr, arow = (uint64_t)r * (uint32_t)T + (uint32_t)tr;
-    const uint8_t *wcp = wc + wrow * (uint32_t)(Kp / 2) + kb * 16, *acp = ac + arow * (uint32_t)(Kp / 2) + kb * 16;
-    const uint8_t *wsp = ws + wrow * (uint32_t)(Kp / 32) + kb, *asp = as + arow * (uint32_t)(Kp / 32) + kb;
-    f32x4 acc = {};
-    for (int k = 0; k < Kp / kMxStepElems; ++k) {
-        acc = mfma_mx(*reinterpret_cast<const u32x4 *>(wcp + k * 64), *reinterpret_cast<const u32x4 *>(acp + k * 64),
-                      acc, wsp[k * 4], asp[k * 4]);
-    }
-    const int t = t0 + row;
-    if (t >= T) return;
-    uint16_t *yr = y + ((uint64_t)r * (uint32_t)T + (uint32_t)t) * (uint32_t)H;
+struct MxArgs {
+    const uint8_t *ac, *as, *wc, *ws;
+    uint16_t *y;
+    int T, H;
+    int stages;                   // of a tile: ceil(Kp / 256)
+    uint32_t code_row, scale_row; // bytes of an operand row: Kp / 2, Kp / 32
+    int tiles_t, tiles_h;
+    uint32_t total;               // tiles of all ranks
+    int grid;
+};
+
+template <int DT, int BH, int BT, int WH, int WT, int NB, int EU>
+__global__ __launch_bounds__(WH *WT * 64) __attribute__((amdgpu_waves_per_eu(EU, EU)))
+void matmul_mxfp4_kernel(const MxArgs p) {
+    constexpr int NW = WH * WT;                    // waves
+    constexpr int SH = BH / WH, ST = BT / WT;      // span of a wave
+    constexpr int NH = SH / 32, NT = ST / 32;      // its blocks
+    constexpr int BR = BH + BT;                    // rows of a stage: w, then a
+    constexpr int RW = BR / NW;                    // rows that a wave stages
+    constexpr int kCodeLoads = RW / 8, kScaleLoads = RW / 32;
+    constexpr int kLoads = kCodeLoads + kScaleLoads;   // per wave and stage
+    constexpr int kCodes = BR * kStageBytes, kScales = BR * kStageScales;
+    static_assert(RW % 32 == 0 && BH % RW == 0, "a wave stages rows of one operand, whole instructions");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[NB * (kCodes + kScales)];
+    uint8_t *const lsc = lds + NB * kCodes;
+
+    const uint32_t tid = __builtin_amdgcn_workitem_id_x();
+    const uint32_t lane = tid & 63u;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(tid >> 6));
+    const int wh = wave % WH, wt = wave / WH;
+
+    // this XCD's run of tiles, and this workgroup's place in it
+    const uint32_t bid = __builtin_amdgcn_workgroup_id_x();
+    const uint32_t xcd = bid % kXcds;
+    const uint32_t base_wgs = (uint32_t)p.grid / kXcds, more_wgs = (uint32_t)p.grid % kXcds;
+    const uint32_t before = xcd * base_wgs + (xcd < more_wgs ? xcd : more_wgs);
+    const uint32_t wgs = base_wgs + (xcd < more_wgs ? 1u : 0u);
+    const uint32_t first = (uint32_t)((uint64_t)p.total * before / (uint32_t)p.grid);
+    const uint32_t last = (uint32_t)((uint64_t)p.total * (before + wgs) / (uint32_t)p.grid);
+
+    struct Tile {
+        uint32_t r, h0, t0;
+    };
+    auto tile_at = [&](uint32_t it, Tile &t) -> bool {
+        const uint32_t logical = first + it * wgs + bid / kXcds;
+        if (logical >= last) return false;
+        const uint32_t per_rank = (uint32_t)p.tiles_t * (uint32_t)p.tiles_h;
+        t.r = logical / per_rank;
+        const uint32_t i = logical - t.r * per_rank;
+        const uint32_t in_full = kGroupT * (uint32_t)p.tiles_h;
+        const uint32_t grp = i / in_full, in_grp = i - grp * in_full;
+        const uint32_t left = (uint32_t)p.tiles_t - grp * kGroupT;
+        const uint32_t gsize = left < kGroupT ? left : kGroupT;
+        t.t0 = (grp * kGroupT + in_grp % gsize) * BT;
+        t.h0 = in_grp / gsize * BH;
+        return true;
+    };
+
+    // --- staging: the load cursor ---
+    const bool on_w = wave * RW < BH;
+    struct Source {
+        const uint8_t *codes, *scales;     // first row that this wave stages
+        uint32_t code_bytes, scale_bytes;  // up to the operand's last row
+    };
+    auto source_of = [&](const Tile &t) {
+        const uint32_t n = on_w ? (uint32_t)p.H : (uint32_t)p.T;           // rows of a rank
+        const uint32_t r0 = on_w ? t.h0 + wave * RW : t.t0 + (wave * RW - BH);
+        const uint64_t g = (uint64_t)t.r * n + (r0 < n ? r0 : 0u);
+        const uint32_t rows = r0 < n ? (n - r0 < (uint32_t)RW ? n - r0 : (uint32_t)RW) : 0u;
+        Source s;
+        s.codes = (on_w ? p.wc : p.ac) + g * p.code_row;
+        s.scales = (on_w ? p.ws : p.as) + g * p.scale_row;
+        s.code_bytes = rows * p.code_row;
+        s.scale_bytes = rows * p.scale_row;
+        return s;
+    };
+    uint32_t lt = 0;          // tile and stage that the next loads fetch
+    int ls = 0;
+    uint32_t lbuf = 0;
+    Tile cur;
+    if (!tile_at(0, cur)) return;
+    Source src = source_of(cur);
+    const bool odd_k = p.code_row % kStageBytes != 0;
+
+    // Loads [from, to) of the cursor's stage. A code load covers 8 rows x 8
+    // chunks, a scale load 32 rows x 2 words. The whole offset is a lane's (the
+    // resource's bounds check covers it), recomputed for every call (`fresh`)
+    // so that none of it is live across the epilogue.
+    auto load_part = [&](int from, int to) {
+        const __amdgpu_buffer_rsrc_t cres = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t *>(src.codes), (short)0, (int)src.code_bytes, kRawBufferFlags);
+        const __amdgpu_buffer_rsrc_t sres = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t *>(src.scales), (short)0, (int)src.scale_bytes, kRawBufferFlags);
+        const bool tail = odd_k && ls + 1 == p.stages;
+        uint8_t *lc = lds + lbuf * kCodes + (uint32_t)wave * (RW * kStageBytes);
+        uint8_t *lw = lsc + lbuf * kScales + (uint32_t)wave * (RW * kStageScales);
+        const uint32_t l = fresh(lane);
+        const uint32_t lrow = l >> 3, lpos = l & 7u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int h = h0 + 4 * kb + j;
-        if (h < H) yr[h] = round1<DT>(acc[j]);
+        for (int j = 0; j < kLoads; ++j) {
+            if (j < from || j >= to) continue;
+            if (j < kCodeLoads) {
+                const uint32_t ch = lpos ^ ((4u * (j & 1) + (lrow >> 1)) & 7u);
+                uint32_t vo = (lrow + 8u * j) * p.code_row + (uint32_t)ls * kStageBytes + (ch << 4);
+                if (tail && ch >= 4u) vo = kPast;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    cres, (__attribute__((address_space(3))) void *)(lc + j * 1024), 16, vo, 0, 0, 0);
+            } else {
+                const int i = j - kCodeLoads;
+                uint32_t vo = ((l >> 1) + 32u * i) * p.scale_row + (uint32_t)ls * kStageScales + (l & 1u) * 4u;
+                if (tail && (l & 1u)) vo = kPast;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    sres, (__attribute__((address_space(3))) void *)(lw + i * 256), 4, vo, 0, 0, 0);
+            }
+        }
+    };
+    // to the next stage of the stream; past the last tile the resources are
+    // empty (the loads still count, and fill buffers that nobody reads)
+    auto load_advance = [&]() {
+        lbuf = lbuf + 1 == NB ? 0 : lbuf + 1;
+        if (++ls == p.stages) {
+            ls = 0;
+            Tile t;
+            if (tile_at(++lt, t)) src = source_of(t);
+            else src.code_bytes = src.scale_bytes = 0;
+        }
+    };
+
+    // --- fragments ---
+    // per-lane offsets within a stage, taken afresh for every tile so that none
+    // of them is live across the epilogue
+    struct Offs {
+        uint32_t ch[4];     // the row's chunk of step ks
+        uint32_t sc, sh;    // its scales, and the shift to this half's byte
+    };
+    auto offs = [&]() {
+        const uint32_t l = fresh(lane);
+        Offs o;
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks)
+            o.ch[ks] = (l & 31u) * kStageBytes + (((2u * ks + (l >> 5)) ^ ((l >> 1) & 7u)) << 4);
+        o.sc = (l & 31u) * kStageScales;
+        o.sh = (l >> 5) * 8u;
+        return o;
+    };
+    uint32_t cbuf = 0;
+    u32x4 fw[2][NH], fa[2][NT];
+    uint32_t sw[2][NH], sa[2][NT];      // scale words of steps 0, 1 and of steps 2, 3
+    auto frag = [&](const Offs &o, uint32_t buf, int ks, int b) {
+        const uint8_t *st = lds + buf * kCodes;
+        if (b < NH) fw[ks & 1][b] = *reinterpret_cast<const u32x4 *>(st + (wh * SH + b * 32) * kStageBytes + o.ch[ks]);
+        if (b < NT) fa[ks & 1][b] = *reinterpret_cast<const u32x4 *>(st + (BH + wt * ST + b * 32) * kStageBytes + o.ch[ks]);
+    };
+    auto scale = [&](const Offs &o, uint32_t buf, int word, int b) {
+        const uint8_t *st = lsc + buf * kScales + word * 4;
+        if (b < NH) sw[word][b] = *reinterpret_cast<const uint32_t *>(st + (wh * SH + b * 32) * kStageScales + o.sc);
+        if (b < NT) sa[word][b] = *reinterpret_cast<const uint32_t *>(st + (BH + wt * ST + b * 32) * kStageScales + o.sc);
+    };
+    auto shift = [&](const Offs &o, int word) {   // a step after the read
+#pragma unroll
+        for (int b = 0; b < NH; ++b) sw[word][b] >>= o.sh;
+#pragma unroll
+        for (int b = 0; b < NT; ++b) sa[word][b] >>= o.sh;
+    };
+    constexpr int NF = NH > NT ? NH : NT;
+
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        load_part(0, kLoads);
+        load_advance();
     }
+    wait_loads<(NB - 1) * kLoads>();
+    barrier_keep_loads();
+#pragma unroll
+    for (int b = 0; b < NF; ++b) {
+        frag(offs(), 0, 0, b);
+        scale(offs(), 0, 0, b);
+    }
+
+    for (uint32_t it = 0;; ++it) {
+        f32x16 acc[NH][NT];
+#pragma unroll
+        for (int a = 0; a < NH; ++a)
+#pragma unroll
+            for (int b = 0; b < NT; ++b) acc[a][b] = f32x16{};
+        auto step = [&](auto ks_, auto &&side) {
+            constexpr int ks = decltype(ks_)::value;
+#pragma unroll
+            for (int nb = 0; nb < NH; ++nb) {
+#pragma unroll
+                for (int tb = 0; tb < NT; ++tb)
+                    acc[nb][tb] = mfma_mx<(ks & 1) * 2>(fw[ks & 1][nb], fa[ks & 1][tb], acc[nb][tb],
+                                                        sw[ks >> 1][nb], sa[ks >> 1][tb]);
+                side(nb);
+                // the accumulators pass through here: without it the compiler
+                // gathers a stage's matrix instructions at its end, with all
+                // of its fragments live
+#pragma unroll
+                for (int tb = 0; tb < NT; ++tb) asm volatile("" : "+v"(acc[nb][tb]));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        const Offs o = offs();
+        // fragment reads of a step's chunk nb, when a wave has more token than channel blocks the rest with the last
+        auto frags = [&](uint32_t buf, int ks, int nb) {
+            frag(o, buf, ks, nb);
+            if (nb == NH - 1)
+                for (int b = NH; b < NF; ++b) frag(o, buf, ks, b);
+        };
+        auto scales = [&](uint32_t buf, int word, int nb) {
+            scale(o, buf, word, nb);
+            if (nb == NH - 1)
+                for (int b = NH; b < NF; ++b) scale(o, buf, word, b);
+        };
+        for (int s = 0; s < p.stages; ++s) {
+            const uint32_t nbuf = cbuf + 1 == NB ? 0 : cbuf + 1;
+            shift(o, 0);
+            step(std::integral_constant<int, 0>{}, [&](int nb) {
+                frags(cbuf, 1, nb);
+                scales(cbuf, 1, nb);
+            });
+            step(std::integral_constant<int, 1>{}, [&](int nb) {
+                frags(cbuf, 2, nb);
+                if (nb == NH - 1) shift(o, 1);
+            });
+            step(std::integral_constant<int, 2>{}, [&](int nb) { frags(cbuf, 3, nb); });
+            // the next stage's loads are done (this wave's; the barrier makes
+            // them everybody's), and every wave has read this stage's last
+            // fragments: its buffer can be filled again
+            wait_loads<(NB - 2) * kLoads>();
+            barrier_keep_loads();
+            step(std::integral_constant<int, 3>{}, [&](int nb) {
+                frags(nbuf, 0, nb);
+                scales(nbuf, 0, nb);
+                load_part(nb * kLoads / NH, (nb + 1) * kLoads / NH);
+            });
+            load_advance();
+            cbuf = nbuf;
+        }
+
+        // epilogue: groups 2 q and 2 q + 1 of 4 channels, swapped between the
+        // halves of the wave, give each lane 8 consecutive channels of a token
+        const uint32_t el = fresh(lane), row = el & 31u, half = el >> 5;
+        uint16_t *const yr = p.y + (uint64_t)cur.r * (uint32_t)p.T * (uint32_t)p.H;
+#pragma unroll
+        for (int tb = 0; tb < NT; ++tb) {
+            const uint32_t t = cur.t0 + (uint32_t)(wt * ST + tb * 32) + row;
+            uint16_t *yt = yr + (uint64_t)t * (uint32_t)p.H;
+#pragma unroll
+            for (int nb = 0; nb < NH; ++nb) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const f32x16 &v = acc[nb][tb];
+                    uint32_t a0 = round2<DT>(v[8 * q + 0], v[8 * q + 1]), a1 = round2<DT>(v[8 * q + 2], v[8 * q + 3]);
+                    uint32_t b0 = round2<DT>(v[8 * q + 4], v[8 * q + 5]), b1 = round2<DT>(v[8 * q + 6], v[8 * q + 7]);
+                    const auto s0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+                    const auto s1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+                    const uint32_t w[4] = {(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
+                    const uint32_t h = cur.h0 + (uint32_t)(wh * SH + nb * 32 + q * 16) + half * 8u;
+                    if (t < (uint32_t)p.T) {
+                        if (h + 8u <= (uint32_t)p.H) {
+                            *reinterpret_cast<u32x4_u16 *>(yt + h) = u32x4{w[0], w[1], w[2], w[3]};
+                        } else {
+#pragma unroll
+                            for (uint32_t k = 0; k < 8; ++k)
+                                if (h + k < (uint32_t)p.H) yt[h + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+                        }
+                    }
+                }
+            }
+        }
+        if (!tile_at(it + 1, cur)) break;
+    }
+    wait_loads<0>();   // nothing may land in LDS after the workgroup has ended
+}
+
+// Compute units of the current device, looked up once per device (atomic:
+// host threads may fill the cache at once, with the same value).
+int compute_units() {
+    static std::atomic<int> cached[64] = {};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return -1;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n <= 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+            n <= 0)
+            return -1;
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <int DT, int BH, int BT, int WH, int WT, int NB, int EU>
+hipError_t launch_tiles(MxArgs p, int R, int per_cu, hipStream_t stream) {
+    p.tiles_t = (p.T + BT - 1) / BT;
+    p.tiles_h = (p.H + BH - 1) / BH;
+    const uint64_t total = (uint64_t)R * (uint64_t)p.tiles_t * (uint64_t)p.tiles_h;
+    const int cus = compute_units();
+    if (cus <= 0) return hipErrorInvalidDevice;
+    if (total > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    p.total = (uint32_t)total;
+    p.grid = (int)(total < (uint64_t)cus * per_cu ? total : (uint64_t)cus * per_cu);
+    hipLaunchKernelGGL((matmul_mxfp4_kernel<DT, BH, BT, WH, WT, NB, EU>), dim3((unsigned)p.grid),
+                       dim3(WH * WT * 64), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t by_shape(const MxArgs &p, int R, hipStream_t stream) {
+    const int cus = compute_units();
+    auto tiles = [&](int b) { return (uint64_t)R * (uint64_t)((p.T + b - 1) / b) * (uint64_t)((p.H + b - 1) / b); };
+    if (tiles(256) >= (uint64_t)cus) return launch_tiles<DT, 256, 256, 2, 4, 2, 2>(p, R, 1, stream);
+    if (tiles(128) >= (uint64_t)cus) return launch_tiles<DT, 128, 128, 2, 2, 4, 1>(p, R, 1, stream);
+    return launch_tiles<DT, 64, 64, 2, 2, 4, 2>(p, R, 2, stream);
 }
 
 }  // namespace
@@ -70,13 +401,18 @@ __global__ __launch_bounds__(kBlockThreads) void matmul_mxfp4_kernel(
 hipError_t launch_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                const uint8_t *w_codes, const uint8_t *w_scales, int R, int T, int Kp,
                                int H, int dtype, uint16_t *y, hipStream_t stream) {
-    const int tiles_t = (T + 15) / 16, tiles_h = (H + 15) / 16;
-    const uint64_t tiles = (uint64_t)R * (uint64_t)tiles_t * (uint64_t)tiles_h;
-    const unsigned blocks = (unsigned)((tiles + kWavesPerBlock - 1) / kWavesPerBlock);
-    auto kernel = dtype == 0 ? matmul_mxfp4_kernel<0> : matmul_mxfp4_kernel<1>;
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kBlockThreads), 0, stream, a_codes, a_scales, w_codes,
-                       w_scales, T, Kp, H, tiles_t, tiles_h, tiles, y);
-    return hipGetLastError();
+    MxArgs p = {};
+    p.ac = a_codes;
+    p.as = a_scales;
+    p.wc = w_codes;
+    p.ws = w_scales;
+    p.y = y;
+    p.T = T;
+    p.H = H;
+    p.stages = (Kp + kStageK - 1) / kStageK;
+    p.code_row = (uint32_t)Kp / 2;
+    p.scale_row = (uint32_t)Kp / kMxBlockElems;
+    return dtype == 0 ? by_shape<0>(p, R, stream) : by_shape<1>(p, R, stream);
 }
 
 }  // namespace fc

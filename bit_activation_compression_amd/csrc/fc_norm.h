@@ -113,7 +113,10 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
     const int H = a.H;
     const uint16_t *res_row = a.residual + row * (uint64_t)H;
 
-    // every operand of the row in flight before the first use
+    // every operand of the row in flight before the first use; rows of more
+    // than 32768 elements would not fit the registers that way, and load all
+    // but x where they use it
+    constexpr bool kEarly = V <= 4;
     float x[V][kLaneElems];
     u32x4 xr[V], rr[V], gr[V], wpost[V], wpre[V];
     uint32_t cw[V][SRC == 8 ? 2 : 1];
@@ -173,20 +176,28 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) xr[v] = load_row8(xrow, (tid + v * NT) * kLaneElems, H);
     }
+    auto elem = [&](int v) { return (tid + v * NT) * kLaneElems; };
+    if constexpr (kEarly) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) rr[v] = load_row8(res_row, (tid + v * NT) * kLaneElems, H);
-    if (a.w_post != nullptr) {
+        for (int v = 0; v < V; ++v) rr[v] = load_row8(res_row, elem(v), H);
+        if (a.w_post != nullptr) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) wpost[v] = load_row8(a.w_post, (tid + v * NT) * kLaneElems, H);
+            for (int v = 0; v < V; ++v) wpost[v] = load_row8(a.w_post, elem(v), H);
+        }
+        if (gate_row != nullptr) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) gr[v] = load_row8(gate_row, elem(v), H);
+        }
+        if (a.w_pre != nullptr) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) wpre[v] = load_row8(a.w_pre, elem(v), H);
+        }
     }
-    if (gate_row != nullptr) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) gr[v] = load_row8(gate_row, (tid + v * NT) * kLaneElems, H);
-    }
-    if (a.w_pre != nullptr) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) wpre[v] = load_row8(a.w_pre, (tid + v * NT) * kLaneElems, H);
-    }
+    // operand vector v, loaded by now or here
+    auto operand = [&](const u32x4 (&early)[V], const uint16_t *row_, int v) {
+        if constexpr (kEarly) return early[v];
+        else return load_row8(row_, elem(v), H);
+    };
 
     // x; elements past the row's end are 0 (codes and scales of 0)
 #pragma unroll
@@ -214,7 +225,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float w[kLaneElems];
-            widen8<DT>(wpost[v], w);
+            widen8<DT>(operand(wpost, a.w_post, v), w);
 #pragma unroll
             for (int k = 0; k < kLaneElems; ++k) x[v][k] = x[v][k] * rstd * w[k];
         }
@@ -223,7 +234,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float g[kLaneElems];
-            widen8<DT>(gr[v], g);
+            widen8<DT>(operand(gr, gate_row, v), g);
 #pragma unroll
             for (int k = 0; k < kLaneElems; ++k) x[v][k] *= g[k];
         }
@@ -234,13 +245,13 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         float r[kLaneElems];
-        widen8<DT>(rr[v], r);
+        widen8<DT>(operand(rr, res_row, v), r);
 #pragma unroll
         for (int k = 0; k < kLaneElems; ++k) {
             x[v][k] = __builtin_fmaf(a.res_scale, r[k], a.out_scale * x[v][k]);
             ss = __builtin_fmaf(x[v][k], x[v][k], ss);
         }
-        store_row8<DT>(hrow, (tid + v * NT) * kLaneElems, H, x[v]);
+        store_row8<DT>(hrow, elem(v), H, x[v]);
     }
     if (a.w_pre == nullptr) return;
     const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(block_sum<NT>(ss, part[1]), a.inv_h, a.eps));
@@ -248,10 +259,10 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         float w[kLaneElems];
-        widen8<DT>(wpre[v], w);
+        widen8<DT>(operand(wpre, a.w_pre, v), w);
 #pragma unroll
         for (int k = 0; k < kLaneElems; ++k) w[k] *= x[v][k] * rstd;
-        store_row8<DT>(yrow, (tid + v * NT) * kLaneElems, H, w);
+        store_row8<DT>(yrow, elem(v), H, w);
     }
 }
 
