@@ -14,7 +14,6 @@ All-Gather, dequantize after it (Figure 5, right; groups as in Figure 4).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -415,12 +414,30 @@ def workspace_views(workspace: torch.Tensor, R: int, T: int, H: int, bits: int, 
 
 
 # --- transformer-block operators (include/fc/layer.h) ------------------------
+# Their calls are often short next to a launch, so the checks of a call that is
+# in order are a few attribute reads; what is wrong is found out afterwards.
 
-def _on(device):
-    """The device's own context: the library launches on the current device. (A
-    no-op object when it is the current one already.)"""
-    return torch.cuda.device(device) if device.index not in (None, torch.cuda.current_device()) \
-        else contextlib.nullcontext()
+# the current device without torch.cuda's lazy-initialization check
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(name: str, device, stream, *args) -> None:
+    """Calls the library on `device` (it launches on the current one) and `stream`."""
+    fn = getattr(_lib or lib(), name)
+    index = device.index
+    if stream is not None:
+        raw = stream.cuda_stream
+    elif _raw_current_stream is not None:
+        raw = _raw_current_stream(index)
+    else:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    if index == _current_device():
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, raw)
+    if st != 0:
+        raise FcError(st, name)
 
 
 def _empty(shape, dtype, device, stream):
@@ -433,42 +450,49 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _like(t: torch.Tensor, name: str, shape, dtype, device) -> None:
-    """An operand of exactly this shape and dtype on `device`."""
+def _like(t: torch.Tensor, name: str, shape: tuple, dtype, device) -> int:
+    """The address of an operand of exactly this shape and dtype on `device`."""
+    if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.is_cuda and t.device == device:
+        return t.data_ptr()
     _dev_tensor(t, name)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
+    raise ValueError(f"{name} must be {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
 
 
 def _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream):
-    """Checks what the block-norm calls share; -> (dtype code, gate_tokens, h, y)."""
+    """Checks what the block-norm calls share; -> (dtype code, the addresses of
+    residual, w_post, gate, then gate_tokens, the addresses of w_pre, h, y, and h, y)."""
     dev, dt = residual.device, residual.dtype
     code = _dt(residual, "residual")
-    _like(residual, "residual", (T, H), dt, dev)
-    if w_post is not None:
-        _like(w_post, "w_post", (H,), dt, dev)
-    if w_pre is not None:
-        _like(w_pre, "w_pre", (H,), dt, dev)
+    rows = (T, H)
+    pr = _like(residual, "residual", rows, dt, dev)
+    pg = py = None
+    pw = None if w_post is None else _like(w_post, "w_post", (H,), dt, dev)
+    pv = None if w_pre is None else _like(w_pre, "w_pre", (H,), dt, dev)
     if gate is not None:
         if gate_tokens is None:
             gate_tokens = max(T, 1) if gate.dim() == 1 else 1
         if gate_tokens < 1:
             raise ValueError(f"gate_tokens must be at least 1, not {gate_tokens}")
-        rows = -(-T // gate_tokens)
-        _like(gate, "gate", (H,) if gate.dim() == 1 and rows <= 1 else (rows, H), dt, dev)
-    if h is None:
-        h = _empty((T, H), dt, dev, stream)
-    _like(h, "h", (T, H), dt, dev)
-    if w_pre is None:
-        if y is not None:
-            raise ValueError("y needs w_pre")
+        n = -(-T // gate_tokens)
+        pg = _like(gate, "gate", (H,) if gate.dim() == 1 and n <= 1 else (n, H), dt, dev)
     else:
+        gate_tokens = 1
+    if h is None:
+        h = torch.empty_like(residual) if stream is None else _empty(rows, dt, dev, stream)
+        ph = h.data_ptr()
+    else:
+        ph = _like(h, "h", rows, dt, dev)
+    if w_pre is not None:
         if y is None:
-            y = _empty((T, H), dt, dev, stream)
-        _like(y, "y", (T, H), dt, dev)
-    return code, gate_tokens or 1, h, y
+            y = torch.empty_like(residual) if stream is None else _empty(rows, dt, dev, stream)
+            py = y.data_ptr()
+        else:
+            py = _like(y, "y", rows, dt, dev)
+    elif y is not None:
+        raise ValueError("y needs w_pre")
+    return code, pr, pw, pg, gate_tokens, pv, ph, py, h, y
 
 
 def fc_residual_norm(x: torch.Tensor, residual: torch.Tensor, w_post=None, w_pre=None, gate=None,
@@ -479,18 +503,14 @@ def fc_residual_norm(x: torch.Tensor, residual: torch.Tensor, w_post=None, w_pre
     -> (h, y), y None without w_pre. w_post and w_pre [H] are RMS-norm weights; without
     w_post x is not normed. gate: [H], or a row for every gate_tokens consecutive tokens
     (default: a row per token). `h` may be `residual` itself (in-place update)."""
-    _dev_tensor(residual, "residual")
     if residual.dim() != 2:
         raise ValueError("residual must be [T, H]")
     T, H = residual.shape
+    code, pr, pw, pg, gate_tokens, pv, ph, py, h, y = _norm_operands(
+        T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
     dev = residual.device
-    _like(x, "x", (T, H), residual.dtype, dev)
-    code, gate_tokens, h, y = _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
-    with _on(dev):
-        st = lib().fc_residual_norm(_ptr(x), _ptr(residual), code, T, H, _ptr(w_post), _ptr(gate),
-                                    gate_tokens, _ptr(w_pre), res_scale, out_scale, eps, _ptr(h),
-                                    _ptr(y), _stream(stream, dev))
-    _check(st, "fc_residual_norm")
+    _launch("fc_residual_norm", dev, stream, _like(x, "x", (T, H), residual.dtype, dev), pr, code, T, H, pw, pg,
+            gate_tokens, pv, res_scale, out_scale, eps, ph, py)
     return h, y
 
 
@@ -501,20 +521,15 @@ def fc_dequantize_residual_norm(codes2, s2, z2, T: int, H: int, bits: int, group
                                 stream=None):
     """fc_residual_norm of the dequantized stage-2 payload (as for fc_dequantize_residual,
     but not rounded to 16 bits before the norms) -> (h, y)."""
-    for n, t in (("codes2", codes2), ("s2", s2), ("z2", z2), ("residual", residual)):
-        _dev_tensor(t, n)
+    code, pr, pw, pg, gate_tokens, pv, ph, py, h, y = _norm_operands(
+        T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
     dev = residual.device
-    code, gate_tokens, h, y = _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
-    _room(codes2, "codes2", T * H * bits // 8, dev)
     meta = T * (H // group2 if group2 > 0 else 0) * 2
+    _room(codes2, "codes2", T * H * bits // 8, dev)
     _room(s2, "s2", meta, dev)
     _room(z2, "z2", meta, dev)
-    with _on(dev):
-        st = lib().fc_dequantize_residual_norm(_ptr(codes2), _ptr(s2), _ptr(z2), T, H, bits, group2,
-                                               code, _ptr(residual), _ptr(w_post), _ptr(gate),
-                                               gate_tokens, _ptr(w_pre), res_scale, out_scale, eps,
-                                               _ptr(h), _ptr(y), _stream(stream, dev))
-    _check(st, "fc_dequantize_residual_norm")
+    _launch("fc_dequantize_residual_norm", dev, stream, codes2.data_ptr(), s2.data_ptr(), z2.data_ptr(), T, H, bits,
+            group2, code, pr, pw, pg, gate_tokens, pv, res_scale, out_scale, eps, ph, py)
     return h, y
 
 
@@ -529,41 +544,39 @@ def fc_allreduce_emulated_norm(x: torch.Tensor, bits: int, group: int, residual:
     R, T, H = x.shape
     dev = x.device
     _like(residual, "residual", (T, H), x.dtype, dev)
-    code, gate_tokens, h, y = _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
+    code, pr, pw, pg, gate_tokens, pv, ph, py, h, y = _norm_operands(
+        T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
     if workspace is None:
         workspace = _empty(max(fc_workspace_bytes(R, T, H, bits, group, bits2), 1), torch.uint8, dev, stream)
     _room(workspace, "workspace", 0, dev)
-    with _on(dev):
-        st = lib().fc_allreduce_emulated_norm(_ptr(x), code, R, T, H, bits, bits2, group, _ptr(residual),
-                                              _ptr(w_post), _ptr(gate), gate_tokens, _ptr(w_pre),
-                                              res_scale, out_scale, eps, _ptr(h), _ptr(y),
-                                              _ptr(workspace),
-                                              workspace.numel() * workspace.element_size(),
-                                              _stream(stream, dev))
-    _check(st, "fc_allreduce_emulated_norm")
+    _launch("fc_allreduce_emulated_norm", dev, stream, x.data_ptr(), code, R, T, H, bits, bits2, group, pr, pw, pg,
+            gate_tokens, pv, res_scale, out_scale, eps, ph, py, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
     return h, y, workspace
 
 
 def _mx_padded(K: int) -> int:
-    return -(-K // 128) * 128
+    return (K + 127) // 128 * 128
 
 
 def _rows3(t: torch.Tensor, name: str):
-    """[R, rows, n] of a 3-D tensor, [1, rows, n] of a 2-D one."""
-    if t.dim() not in (2, 3):
+    """(R, rows, n) of a 3-D tensor, (1, rows, n) of a 2-D one."""
+    s = t.shape
+    if len(s) == 3:
+        return s
+    if len(s) != 2:
         raise ValueError(f"{name} must have 2 or 3 dimensions")
-    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+    return 1, s[0], s[1]
 
 
 def _mx_operand(codes, scales, name: str, device):
-    """MXFP4 codes [..., rows, Kp/2] with scales [..., rows, Kp/32] -> (R, rows, Kp)."""
-    _dev_tensor(codes, f"{name}codes")
-    R, rows, half = _rows3(codes, f"{name}codes")
+    """MXFP4 codes [..., rows, Kp/2] with scales [..., rows, Kp/32] -> (R, rows, Kp, their addresses)."""
+    s = codes.shape
+    R, rows, half = _rows3(codes, name + "codes")
     if half == 0 or half % 64 != 0:
         raise ValueError(f"{name}codes must hold a positive multiple of 64 bytes a row, not {half}")
-    _like(codes, f"{name}codes", codes.shape, torch.uint8, device)
-    _like(scales, f"{name}scales", (*codes.shape[:-1], half // 16), torch.uint8, device)
-    return R, rows, 2 * half
+    return (R, rows, 2 * half, _like(codes, name + "codes", s, torch.uint8, device),
+            _like(scales, name + "scales", (*s[:-1], half // 16), torch.uint8, device))
 
 
 def fc_quantize_mxfp4(x: torch.Tensor, codes=None, scales=None, stream=None):
@@ -571,63 +584,57 @@ def fc_quantize_mxfp4(x: torch.Tensor, codes=None, scales=None, stream=None):
     [..., Kp/32]) uint8, Kp = K rounded up to a multiple of 128 (the padding is zeros)."""
     _dev_tensor(x, "x")
     R, T, K = _rows3(x, "x")
-    dev, Kp = x.device, _mx_padded(K)
+    dev, Kp, lead = x.device, _mx_padded(K), x.shape[:-1]
     if codes is None:
-        codes = _empty((*x.shape[:-1], Kp // 2), torch.uint8, dev, stream)
+        codes = _empty((*lead, Kp // 2), torch.uint8, dev, stream)
+        pc = codes.data_ptr()
+    else:
+        pc = _like(codes, "codes", (*lead, Kp // 2), torch.uint8, dev)
     if scales is None:
-        scales = _empty((*x.shape[:-1], Kp // 32), torch.uint8, dev, stream)
-    _like(codes, "codes", (*x.shape[:-1], Kp // 2), torch.uint8, dev)
-    _like(scales, "scales", (*x.shape[:-1], Kp // 32), torch.uint8, dev)
-    with _on(dev):
-        st = lib().fc_quantize_mxfp4(_ptr(x), _dt(x, "x"), R, T, K, _ptr(codes), _ptr(scales),
-                                     _stream(stream, dev))
-    _check(st, "fc_quantize_mxfp4")
+        scales = _empty((*lead, Kp // 32), torch.uint8, dev, stream)
+        ps = scales.data_ptr()
+    else:
+        ps = _like(scales, "scales", (*lead, Kp // 32), torch.uint8, dev)
+    _launch("fc_quantize_mxfp4", dev, stream, x.data_ptr(), _dt(x, "x"), R, T, K, pc, ps)
     return codes, scales
 
 
 def fc_dequantize_mxfp4(codes, scales, K: int, dtype: torch.dtype, out=None, stream=None):
     """MXFP4 codes [..., Kp/2] and scales [..., Kp/32] -> out [..., K] of `dtype`."""
-    _dev_tensor(codes, "codes")
     dev = codes.device
-    R, T, Kp = _mx_operand(codes, scales, "", dev)
+    R, T, Kp, pc, ps = _mx_operand(codes, scales, "", dev)
     if K < 1 or _mx_padded(K) != Kp:
         raise ValueError(f"codes hold rows of {Kp} values, K is {K}")
+    shape = (*codes.shape[:-1], K)
     if out is None:
-        out = _empty((*codes.shape[:-1], K), dtype, dev, stream)
-    _like(out, "out", (*codes.shape[:-1], K), dtype, dev)
-    with _on(dev):
-        st = lib().fc_dequantize_mxfp4(_ptr(codes), _ptr(scales), R, T, K, _dt(out, "out"), _ptr(out),
-                                       _stream(stream, dev))
-    _check(st, "fc_dequantize_mxfp4")
+        out = _empty(shape, dtype, dev, stream)
+        po = out.data_ptr()
+    else:
+        po = _like(out, "out", shape, dtype, dev)
+    _launch("fc_dequantize_mxfp4", dev, stream, pc, ps, R, T, K, _dt(out, "out"), po)
     return out
-
-
-def _product_out(y, lead, T, H, dtype, device, stream):
-    if y is None:
-        y = _empty((*lead, T, H), dtype, device, stream)
-    _like(y, "y", (*lead, T, H), dtype, device)
-    return y
 
 
 def fc_matmul_mxfp4(a_codes, a_scales, w_codes, w_scales, dtype: torch.dtype, y=None, stream=None):
     """MXFP4 a [R, T, K] and w [R, H, K] (or both without R) -> y [R, T, H] = a @ w^T of
     `dtype`, accumulated in binary32."""
-    _dev_tensor(a_codes, "a_codes")
     dev = a_codes.device
-    R, T, Kp = _mx_operand(a_codes, a_scales, "a_", dev)
-    Rw, H, Kw = _mx_operand(w_codes, w_scales, "w_", dev)
-    if (R, Kp, a_codes.dim()) != (Rw, Kw, w_codes.dim()):
+    R, T, Kp, pa, pas = _mx_operand(a_codes, a_scales, "a_", dev)
+    Rw, H, Kw, pw, pws = _mx_operand(w_codes, w_scales, "w_", dev)
+    if R != Rw or Kp != Kw or a_codes.dim() != w_codes.dim():
         raise ValueError("a must be [R, T, K] and w [R, H, K]")
-    y = _product_out(y, a_codes.shape[:-2], T, H, dtype, dev, stream)
-    with _on(dev):
-        st = lib().fc_matmul_mxfp4(_ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), R, T, Kp,
-                                   H, _dt(y, "y"), _ptr(y), _stream(stream, dev))
-    _check(st, "fc_matmul_mxfp4")
+    shape = (*a_codes.shape[:-1], H)
+    if y is None:
+        y = _empty(shape, dtype, dev, stream)
+        py = y.data_ptr()
+    else:
+        py = _like(y, "y", shape, dtype, dev)
+    _launch("fc_matmul_mxfp4", dev, stream, pa, pas, pw, pws, R, T, Kp, H, _dt(y, "y"), py)
     return y
 
 
 def fc_linear_mxfp4_workspace_bytes(R: int, T: int, K: int) -> int:
-    return lib().fc_linear_mxfp4_workspace_bytes(R, T, K)
+    return (_lib or lib()).fc_linear_mxfp4_workspace_bytes(R, T, K)
 
 
 def fc_linear_mxfp4(a: torch.Tensor, w_codes, w_scales, y=None, workspace=None, stream=None):
@@ -636,19 +643,23 @@ def fc_linear_mxfp4(a: torch.Tensor, w_codes, w_scales, y=None, workspace=None, 
     _dev_tensor(a, "a")
     R, T, K = _rows3(a, "a")
     dev = a.device
-    Rw, H, Kw = _mx_operand(w_codes, w_scales, "w_", dev)
-    if (R, _mx_padded(K), a.dim()) != (Rw, Kw, w_codes.dim()):
+    Rw, H, Kw, pw, pws = _mx_operand(w_codes, w_scales, "w_", dev)
+    if R != Rw or _mx_padded(K) != Kw or a.dim() != w_codes.dim():
         raise ValueError("a must be [R, T, K] and w [R, H, K]")
-    y = _product_out(y, a.shape[:-2], T, H, a.dtype, dev, stream)
-    need = fc_linear_mxfp4_workspace_bytes(R, T, K)
-    if workspace is None and need:
-        workspace = _empty(need, torch.uint8, dev, stream)
-    have = 0
-    if workspace is not None:
+    shape = (*a.shape[:-1], H)
+    if y is None:
+        y = _empty(shape, a.dtype, dev, stream)
+        py = y.data_ptr()
+    else:
+        py = _like(y, "y", shape, a.dtype, dev)
+    have, pk = 0, None
+    if workspace is None:
+        need = fc_linear_mxfp4_workspace_bytes(R, T, K)
+        if need:
+            workspace = _empty(need, torch.uint8, dev, stream)
+            have, pk = need, workspace.data_ptr()
+    else:
         _room(workspace, "workspace", 0, dev)
-        have = workspace.numel() * workspace.element_size()
-    with _on(dev):
-        st = lib().fc_linear_mxfp4(_ptr(a), _ptr(w_codes), _ptr(w_scales), _dt(a, "a"), R, T, K, H, _ptr(y),
-                                   _ptr(workspace), have, _stream(stream, dev))
-    _check(st, "fc_linear_mxfp4")
+        have, pk = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    _launch("fc_linear_mxfp4", dev, stream, a.data_ptr(), pw, pws, _dt(a, "a"), R, T, K, H, py, pk, have)
     return y

@@ -10,11 +10,12 @@
 // 16-bit block output, 6.5 from an INT4 payload. Everything between the loads
 // and the two final roundings is binary32.
 //
-// A row is NT threads x V vectors of 8 elements (thread i holds vectors i, i +
-// NT, ...), so a wave's load covers 1 KiB of consecutive elements. Rows need
-// no alignment beyond an element's: the vectors are loaded and stored at
-// 2-byte alignment (one global_load_dwordx4 all the same), and only a row's
-// last vector, when H is not a multiple of 8, goes element by element.
+// A row is NT threads (whole waves, as many as it needs) x V vectors of 8
+// elements (thread i holds vectors i, i + NT, ...), so a wave's load covers
+// 1 KiB of consecutive elements. Rows need
+// no alignment beyond an element's: vectors are loaded and stored at 2-byte
+// alignment (one global_load_dwordx4 all the same), and the last vector of a
+// row that is no whole number of them loads the row's last 8 elements.
 #pragma once
 
 #include "fc_device.h"
@@ -23,20 +24,28 @@
 namespace fc {
 namespace {
 
+constexpr int kNormThreads = 1024;   // most of a workgroup
+constexpr uint64_t kManyElems = uint64_t(1) << 23;
+constexpr uint64_t kInfinityCache = uint64_t(256) << 20;
+
 // vectors at the alignment of their elements
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
 
-// Sum over the wave, the same in every lane: xor butterflies inside a row of
-// 16 lanes (every lane adds the same pairs), then the four rows' sums in a
-// fixed order.
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over rows of 16 lanes, the same bits in every lane of a row: butterflies
+// in which both partners add the same pair.
+__device__ __forceinline__ float row_sum(float v) {
     v += dpp<0xB1>(v);    // lane ^ 1
     v += dpp<0x4E>(v);    // lane ^ 2
     v += dpp<0x141>(v);   // 7 - i inside 8 lanes
     v += dpp<0x140>(v);   // 15 - i inside 16 lanes
-    const int b = __builtin_bit_cast(int, v);
+    return v;
+}
+
+// Sum over the wave: the four rows' sums in a fixed order.
+__device__ __forceinline__ float wave_sum(float v) {
+    const int b = __builtin_bit_cast(int, row_sum(v));
     const float a0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0));
     const float a1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));
     const float a2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));
@@ -44,19 +53,17 @@ __device__ __forceinline__ float wave_sum(float v) {
     return (a0 + a1) + (a2 + a3);
 }
 
-// Sum over the workgroup, the same bits in every thread. `part` is this
-// reduction's own LDS (one float per wave): no barrier is needed after it.
-template <int NT>
-__device__ __forceinline__ float block_sum(float v, float *part) {
-    constexpr int NW = NT / kWave;
+// Sum over the workgroup's nw <= 16 waves, the same bits in every thread.
+// `part` is this reduction's own LDS (one float per wave): no barrier is
+// needed after it.
+__device__ __forceinline__ float block_sum(float v, float *part, uint32_t nw) {
     v = wave_sum(v);
-    if constexpr (NW > 1) {
-        const uint32_t tid = __builtin_amdgcn_workitem_id_x();
+    if (nw > 1) {
+        const uint32_t tid = __builtin_amdgcn_workitem_id_x(), i = tid & 15u;
         if ((tid & (kWave - 1)) == 0) part[tid / kWave] = v;
         __syncthreads();
-        v = part[0];
-#pragma unroll
-        for (int i = 1; i < NW; ++i) v += part[i];
+        v = i < nw ? part[i] : 0.0f;
+        v = row_sum(v);
     }
     return v;
 }
@@ -73,25 +80,29 @@ __device__ __forceinline__ uint16_t narrow1(float v) {
     else return __builtin_bit_cast(uint16_t, (_Float16)as_f32(v));
 }
 
-// 8 elements from e of a row of H; zeros past its end.
-__device__ __forceinline__ u32x4 load_row8(const uint16_t *row, int e, int H) {
-    if (e + kLaneElems <= H) return *reinterpret_cast<const u32x4_a2 *>(row + e);
+// The 8 elements from b of a row of H; of a row shorter than that, those it has.
+__device__ __forceinline__ u32x4 load_row8(const uint16_t *row, int b, int H) {
+    if (H >= kLaneElems) return *reinterpret_cast<const u32x4_a2 *>(row + b);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < kLaneElems; ++k)
-        if (e + k < H) w[k / 2] |= (uint32_t)row[e + k] << (16 * (k & 1));
+        if (k < H) w[k / 2] |= (uint32_t)row[k] << (16 * (k & 1));
     return u32x4{w[0], w[1], w[2], w[3]};
 }
 
+// v[k] is element b + k; the lane's own are those from e to the row's end.
 template <int DT>
-__device__ __forceinline__ void store_row8(uint16_t *row, int e, int H, const float (&v)[kLaneElems]) {
+__device__ __forceinline__ void store_row8(uint16_t *row, int e, int b, int H, bool past_cache,
+                                           const float (&v)[kLaneElems]) {
     if (e + kLaneElems <= H) {
-        *reinterpret_cast<u32x4_a2 *>(row + e) = narrow8<DT>(v);
+        u32x4_a2 *p = reinterpret_cast<u32x4_a2 *>(row + e);
+        if (past_cache) __builtin_nontemporal_store(narrow8<DT>(v), p);
+        else *p = narrow8<DT>(v);
         return;
     }
 #pragma unroll
     for (int k = 0; k < kLaneElems; ++k)
-        if (e + k < H) row[e + k] = narrow1<DT>(v[k]);
+        if (b + k >= e && b + k < H) row[b + k] = narrow1<DT>(v[k]);
 }
 
 // n / d by the reciprocal ceil(2^32 / d), exact while n * d < 2^32; 0 stands
@@ -105,12 +116,25 @@ __device__ __forceinline__ uint32_t group_of(uint32_t n, uint32_t magic) {
 // inside a vector (at a pair: groups are even); otherwise a vector lies in one
 // group. A group's number is that of the vector (pair) over the vectors
 // (pairs) of a group, both at most 2^15.
-template <int DT, int SRC, bool GEN, int NT, int V>
-__global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
-    __shared__ float part[2][NT / kWave];
+template <int DT, int SRC, bool GEN, int V>
+__global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormArgs a) {
+    __shared__ float part[2][kNormThreads / kWave];
+    const int NT = a.waves * kWave;
     const int tid = (int)__builtin_amdgcn_workitem_id_x();
     const uint64_t row = __builtin_amdgcn_workgroup_id_x();
     const int H = a.H;
+    // Vector v of the thread: its elements are those from elem(v), if any. All
+    // loads take 8 whole ones, from begin(v): the row's last 8 where fewer (or
+    // none) are left, and `own` zeroes what is not the thread's own.
+    auto elem = [&](int v) { return (tid + v * NT) * kLaneElems; };
+    const int last = H > kLaneElems ? H - kLaneElems : 0;
+    auto begin = [&](int v) { return elem(v) < last ? elem(v) : last; };
+    auto own = [&](int v, float (&x)[kLaneElems]) {
+        if (elem(v) + kLaneElems <= H) return;
+#pragma unroll
+        for (int k = 0; k < kLaneElems; ++k)
+            if (begin(v) + k < elem(v) || begin(v) + k >= H) x[k] = 0.0f;
+    };
     const uint16_t *res_row = a.residual + row * (uint64_t)H;
 
     // every operand of the row in flight before the first use; rows of more
@@ -124,84 +148,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
     const uint16_t *gate_row = nullptr;
     if (a.gate != nullptr)
         gate_row = a.gate + (uint64_t)((uint32_t)row / (uint32_t)a.gate_tokens) * (uint64_t)H;
-    if constexpr (SRC != 0) {
-        const uint8_t *crow = a.codes + row * (uint64_t)H * SRC / 8;
-        const uint64_t g0 = row * (uint64_t)a.groups;
-        const uint16_t *srow = a.s + g0, *zrow = a.z + g0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int i = tid + v * NT, e = i * kLaneElems;
-#pragma unroll
-            for (uint32_t &w : cw[v]) w = 0;
-#pragma unroll
-            for (uint32_t &w : sz[v]) w = 0;
-            if (e + kLaneElems <= H) {
-                if constexpr (SRC == 4) {
-                    cw[v][0] = *reinterpret_cast<const u32_a1 *>(crow + e / 2);
-                } else {
-                    const u32x2 w = *reinterpret_cast<const u32x2_a1 *>(crow + e);
-                    cw[v][0] = w.x;
-                    cw[v][1] = w.y;
-                }
-            } else if constexpr (GEN) {
-                // the row's last vector: whole pairs (H is even with a payload;
-                // with groups of whole vectors it is a multiple of 8)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    if (e + 2 * p < H) {
-                        if constexpr (SRC == 4) {
-                            cw[v][0] |= (uint32_t)crow[e / 2 + p] << (8 * p);
-                        } else {
-                            cw[v][p / 2] |= ((uint32_t)crow[e + 2 * p] | (uint32_t)crow[e + 2 * p + 1] << 8)
-                                            << (16 * (p & 1));
-                        }
-                    }
-                }
-            }
-            if constexpr (GEN) {
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    if (e + 2 * p < H) {
-                        const uint32_t g = group_of((uint32_t)(i * 4 + p), a.gmagic);
-                        sz[v][p] = (uint32_t)srow[g] | (uint32_t)zrow[g] << 16;
-                    }
-                }
-            } else if (e < H) {
-                const uint32_t g = group_of((uint32_t)i, a.gmagic);
-                sz[v][0] = (uint32_t)srow[g] | (uint32_t)zrow[g] << 16;
-            }
-        }
-    } else {
-        const uint16_t *xrow = a.x + row * (uint64_t)H;
-#pragma unroll
-        for (int v = 0; v < V; ++v) xr[v] = load_row8(xrow, (tid + v * NT) * kLaneElems, H);
-    }
-    auto elem = [&](int v) { return (tid + v * NT) * kLaneElems; };
-    if constexpr (kEarly) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) rr[v] = load_row8(res_row, elem(v), H);
-        if (a.w_post != nullptr) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) wpost[v] = load_row8(a.w_post, elem(v), H);
-        }
-        if (gate_row != nullptr) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) gr[v] = load_row8(gate_row, elem(v), H);
-        }
-        if (a.w_pre != nullptr) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) wpre[v] = load_row8(a.w_pre, elem(v), H);
-        }
-    }
-    // operand vector v, loaded by now or here
-    auto operand = [&](const u32x4 (&early)[V], const uint16_t *row_, int v) {
-        if constexpr (kEarly) return early[v];
-        else return load_row8(row_, elem(v), H);
-    };
-
-    // x; elements past the row's end are 0 (codes and scales of 0)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
+    auto to_x = [&](int v) {
         if constexpr (SRC == 0) {
             widen8<DT>(xr[v], x[v]);
         } else {
@@ -213,6 +160,75 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
                                          half_bits_to_float((uint16_t)(m >> 16)));
             }
         }
+        own(v, x[v]);
+    };
+    if constexpr (SRC != 0) {
+        const uint8_t *crow = a.codes + row * (uint64_t)H * SRC / 8;
+        const uint64_t g0 = row * (uint64_t)a.groups;
+        const uint16_t *srow = a.s + g0, *zrow = a.z + g0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int b = begin(v);
+            if (!GEN || H >= kLaneElems) {
+                if constexpr (SRC == 4) {
+                    cw[v][0] = *reinterpret_cast<const u32_a1 *>(crow + b / 2);
+                } else {
+                    const u32x2 w = *reinterpret_cast<const u32x2_a1 *>(crow + b);
+                    cw[v][0] = w.x;
+                    cw[v][1] = w.y;
+                }
+            } else {
+                for (uint32_t &w : cw[v]) w = 0;
+#pragma unroll
+                for (int k = 0; k < kLaneElems * SRC / 8; ++k)
+                    if (k < H * SRC / 8) cw[v][k / 4] |= (uint32_t)crow[k] << (8 * (k & 3));
+            }
+            if constexpr (GEN) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const uint32_t pair = (uint32_t)(b / 2 + p);
+                    const uint32_t g = group_of(pair < (uint32_t)H / 2 ? pair : 0u, a.gmagic);
+                    sz[v][p] = (uint32_t)srow[g] | (uint32_t)zrow[g] << 16;
+                }
+            } else {
+                const uint32_t g = group_of((uint32_t)b / kLaneElems, a.gmagic);
+                sz[v][0] = (uint32_t)srow[g] | (uint32_t)zrow[g] << 16;
+            }
+            if constexpr (!kEarly) {
+                to_x(v);   // one vector's codes and scales at a time
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    } else {
+        const uint16_t *xrow = a.x + row * (uint64_t)H;
+#pragma unroll
+        for (int v = 0; v < V; ++v) xr[v] = load_row8(xrow, begin(v), H);
+    }
+    if constexpr (kEarly) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) rr[v] = load_row8(res_row, begin(v), H);
+        if (a.w_post != nullptr) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) wpost[v] = load_row8(a.w_post, begin(v), H);
+        }
+        if (gate_row != nullptr) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) gr[v] = load_row8(gate_row, begin(v), H);
+        }
+        if (a.w_pre != nullptr) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) wpre[v] = load_row8(a.w_pre, begin(v), H);
+        }
+    }
+    // operand vector v, loaded by now or here
+    auto operand = [&](const u32x4 (&early)[V], const uint16_t *row_, int v) {
+        if constexpr (kEarly) return early[v];
+        else return load_row8(row_, begin(v), H);
+    };
+
+    if constexpr (SRC == 0 || kEarly) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) to_x(v);
     }
 
     if (a.w_post != nullptr) {
@@ -221,7 +237,7 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int k = 0; k < kLaneElems; ++k) ss = __builtin_fmaf(x[v][k], x[v][k], ss);
-        const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(block_sum<NT>(ss, part[0]), a.inv_h, a.eps));
+        const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(block_sum(ss, part[0], (uint32_t)a.waves), a.inv_h, a.eps));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float w[kLaneElems];
@@ -249,12 +265,14 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int k = 0; k < kLaneElems; ++k) {
             x[v][k] = __builtin_fmaf(a.res_scale, r[k], a.out_scale * x[v][k]);
-            ss = __builtin_fmaf(x[v][k], x[v][k], ss);
         }
-        store_row8<DT>(hrow, elem(v), H, x[v]);
+        own(v, x[v]);
+#pragma unroll
+        for (int k = 0; k < kLaneElems; ++k) ss = __builtin_fmaf(x[v][k], x[v][k], ss);
+        store_row8<DT>(hrow, elem(v), begin(v), H, a.past_cache, x[v]);
     }
     if (a.w_pre == nullptr) return;
-    const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(block_sum<NT>(ss, part[1]), a.inv_h, a.eps));
+    const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(block_sum(ss, part[1], (uint32_t)a.waves), a.inv_h, a.eps));
     uint16_t *yrow = a.y + row * (uint64_t)H;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -262,24 +280,33 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
         widen8<DT>(operand(wpre, a.w_pre, v), w);
 #pragma unroll
         for (int k = 0; k < kLaneElems; ++k) w[k] *= x[v][k] * rstd;
-        store_row8<DT>(yrow, elem(v), H, w);
+        store_row8<DT>(yrow, elem(v), begin(v), H, a.past_cache, w);
     }
 }
 
-template <int DT, int SRC, bool GEN, int NT, int V>
-hipError_t launch_norm_rows(const NormArgs &a, hipStream_t stream) {
-    hipLaunchKernelGGL((norm_kernel<DT, SRC, GEN, NT, V>), dim3((unsigned)a.T), dim3(NT), 0, stream, a);
+template <int DT, int SRC, bool GEN, int V>
+hipError_t launch_norm_rows(NormArgs a, int nv, hipStream_t stream) {
+    a.waves = (nv + V * kWave - 1) / (V * kWave);
+    hipLaunchKernelGGL((norm_kernel<DT, SRC, GEN, V>), dim3((unsigned)a.T), dim3((unsigned)(a.waves * kWave)),
+                       0, stream, a);
     return hipGetLastError();
 }
 
 template <int DT, int SRC, bool GEN>
-hipError_t launch_norm_any(const NormArgs &a, hipStream_t stream) {
+hipError_t launch_norm_any(NormArgs a, hipStream_t stream) {
     const int nv = (a.H + kLaneElems - 1) / kLaneElems;   // vectors of a row
-    if (nv <= 64) return launch_norm_rows<DT, SRC, GEN, 64, 1>(a, stream);
-    if (nv <= 256) return launch_norm_rows<DT, SRC, GEN, 256, 1>(a, stream);
-    if (nv <= 1024) return launch_norm_rows<DT, SRC, GEN, 1024, 1>(a, stream);
-    if (nv <= 4096) return launch_norm_rows<DT, SRC, GEN, 1024, 4>(a, stream);
-    return launch_norm_rows<DT, SRC, GEN, 1024, 8>(a, stream);
+    // Outputs that the Infinity Cache cannot hold for their readers are written
+    // past it: 8192 x 8192 from an INT4 payload 79 -> 76 us, 4096 x 16384 99 -> 95;
+    // outputs that fit it are faster through it (8192 x 4096: 43 against 48).
+    a.past_cache = (uint64_t)a.T * (uint64_t)a.H * (a.y ? 4 : 2) > kInfinityCache;
+    // Two vectors per thread once the device is full of rows: H = 8192 bf16,
+    // 512 / 1024 / 2048 rows 9.2 / 12.7 / 24.1 us against 9.0 / 14.2 / 24.6 with
+    // one; H = 4096, 512 / 1024 / 8192 rows 5.6 / 9.0 / 43.0 against 5.5 / 8.7 / 44.5.
+    const bool few = (uint64_t)a.T * (uint64_t)a.H < kManyElems;
+    if (nv <= kNormThreads && few) return launch_norm_rows<DT, SRC, GEN, 1>(a, nv, stream);
+    if (nv <= 2 * kNormThreads) return launch_norm_rows<DT, SRC, GEN, 2>(a, nv, stream);
+    if (nv <= 4 * kNormThreads) return launch_norm_rows<DT, SRC, GEN, 4>(a, nv, stream);
+    return launch_norm_rows<DT, SRC, GEN, 8>(a, nv, stream);
 }
 
 }  // namespace
