@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["fc_api.hip", "fc_quantize.hip", "fc_dequant_sum_requant.hip", "fc_dequantize.hip",
            "fc_sum.hip", "fc_linear_quantize.hip", "fc_allreduce_small.hip", "fc_stream.hip",
            "fc_generic.hip", "fc_residual_norm.hip", "fc_dequantize_residual_norm.hip",
-           "fc_mxfp4.hip", "fc_matmul_mxfp4.hip"]
+           "fc_mxfp4.hip", "fc_matmul_mxfp4.hip",
+           "fc_matmul_mxfp4_few.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -439,15 +439,20 @@ fc_status fc_linear_mxfp4(const void *a, const uint8_t *w_codes, const uint8_t *
     fc_status st = check_mx_product(R, T, K, H);
     if (st != FC_OK) return st;
     if (dt != FC_F16 && dt != FC_BF16) return FC_ERR_DTYPE;
-    st = check_ptrs((size_t)T, {a, w_codes, w_scales, y, workspace});
-    if (st != FC_OK || T == 0) return st;
     const size_t need = fc_linear_mxfp4_workspace_bytes(R, T, K);
+    st = need ? check_ptrs((size_t)T, {a, w_codes, w_scales, y, workspace})
+              : check_ptrs((size_t)T, {a, w_codes, w_scales, y});
+    if (st != FC_OK || T == 0) return st;
     if (workspace_bytes < need) return FC_ERR_WORKSPACE;
     st = check_overlap({{y, (size_t)R * (size_t)T * (size_t)H * 2}, {workspace, need}},
                        {{a, (size_t)R * (size_t)T * (size_t)K * 2},
                         {w_codes, mx_code_bytes(R, H, K)}, {w_scales, mx_scale_bytes(R, H, K)}});
     if (st != FC_OK) return st;
     const int Kp = (int)mx_padded(K);
+    if (need == 0)
+        return from_hip(fc::launch_linear_mxfp4_few(static_cast<const uint16_t *>(a), w_codes, w_scales, R, T,
+                                                    K, Kp, H, (int)dt, static_cast<uint16_t *>(y),
+                                                    static_cast<hipStream_t>(stream)));
     uint8_t *codes = static_cast<uint8_t *>(workspace);
     uint8_t *scales = codes + mx_workspace_scales(R, T, K);
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -459,7 +464,8 @@ fc_status fc_linear_mxfp4(const void *a, const uint8_t *w_codes, const uint8_t *
 }
 
 size_t fc_linear_mxfp4_workspace_bytes(int R, int T, int K) {
-    if (check_mx(R, T, K) != FC_OK || T == 0) return 0;
+    if (check_mx(R, T, K) != FC_OK || T == 0 || fc::mxfp4_quantizes_in_place(T, (int)mx_padded(K)))
+        return 0;
     return mx_workspace_scales(R, T, K) + mx_scale_bytes(R, T, K);
 }
 

@@ -100,5 +100,20 @@ hipError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, 
 hipError_t launch_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                const uint8_t *w_codes, const uint8_t *w_scales, int R, int T, int Kp,
                                int H, int dtype, uint16_t *y, hipStream_t stream);
+// The same for at most kMxFewTokens tokens and fewer than kMxFewChannels
+// channels of all ranks (launch_matmul_mxfp4 chooses), which would not fill the
+// device with tiles. us against tiles, bf16; R, T, K, H: 1, 16, 4096, 4096 6.2 /
+// 10.0; 1, 64, 4096, 4096 9.8 / 10.6; 4, 16, 2048, 8192 13.3 / 10.2.
+constexpr int kMxFewTokens = 64;
+constexpr uint64_t kMxFewChannels = 16384;
+hipError_t launch_matmul_mxfp4_few(const uint8_t *a_codes, const uint8_t *a_scales,
+                                   const uint8_t *w_codes, const uint8_t *w_scales, int R, int T, int Kp,
+                                   int H, int dtype, uint16_t *y, hipStream_t stream);
+// The product of 16-bit activations a [R][T][K], quantized in the kernel, for
+// calls with few of them (mxfp4_quantizes_in_place).
+bool mxfp4_quantizes_in_place(int T, int Kp);
+hipError_t launch_linear_mxfp4_few(const uint16_t *a, const uint8_t *w_codes, const uint8_t *w_scales,
+                                   int R, int T, int K, int Kp, int H, int dtype, uint16_t *y,
+                                   hipStream_t stream);
 
 }  // namespace fc

@@ -8,23 +8,42 @@
 // Work layout:
 //   - a workgroup owns a BH (channels) x BT (tokens) tile of one rank's
 //     output, its WH x WT waves (BH / WH) x (BT / WT) each, in 32 x 32 blocks;
-//   - K is walked in stages of 256 (128 bytes of codes and 8 of scales a row,
-//     whole L2 lines), NB of them in LDS, filled straight from global memory
-//     (buffer_load ... lds) NB - 1 stages ahead. The eight 16-byte chunks of a
-//     row are rotated by (row / 2) % 8, so that a fragment read (32 rows x one
-//     chunk) is free of bank conflicts;
+//   - K is walked in stages of 256: 128 bytes of codes (a whole line) and 8 of
+//     scales a row. NB stages are held in LDS, filled straight from global
+//     memory (buffer_load ... lds) as soon as a buffer is free. The eight
+//     16-byte chunks of a row are rotated by (row / 2) % 8, so that a fragment
+//     read (32 rows x one chunk) is free of bank conflicts;
+//   - the scales are fetched 16 bytes a row at a time, for 2 stages: a load of
+//     8 bytes a row touches as many lines for half the use, and that way the
+//     scales cost the cache more accesses than the codes (70B d_proj slices
+//     1.08 -> 1.03 ms);
 //   - a stage is 4 matrix-core steps of k = 64. Step ks takes blocks 2 ks (lanes
-//     0..31) and 2 ks + 1 (lanes 32..63) of each row: the scale bytes of a row
-//     are read as two words, shifted right by a byte in the upper lanes, and
-//     the instruction's byte selection picks byte 0 or 2;
-//   - rows past H or T, and the second half of the last stage where K is an odd
-//     multiple of 128, lie past the buffer resources and read as zeros;
+//     0..31) and 2 ks + 1 (lanes 32..63) of each row: the scale words of a row
+//     (one for steps 0 and 1, one for 2 and 3) are shifted right by a byte in
+//     the upper lanes, and the instruction's byte selection picks byte 0 or 2;
+//   - small tiles read a stage's fragments from LDS while they multiply the
+//     stage before (their few matrix instructions would not cover the latency
+//     of reads a step ahead); large ones, short of registers, read a step ahead;
+//   - rows past H or T lie past the buffer resources and read as zeros. Where K
+//     is an odd multiple of 128, the second half of the last stage is not
+//     fetched (zeros again) and gets scales of 0;
 //   - workgroups are persistent: stages of consecutive tiles form one stream,
 //     so the next tile's first stages are in flight during a tile's epilogue.
 //     The tiles are split into one contiguous run per XCD (workgroup b runs on
 //     XCD b % 8), in groups of 4 token tiles x all channel tiles, so that the
 //     workgroups of an XCD share operands in its L2.
+//
+// What bounds it: the large tile's matrix instructions alone run at 5.3 PFLOP/s
+// with all compute units on random operands (9.8 without the toggling: the
+// power management lowers the clock), and LDS traffic (96 KiB of fragment
+// reads and 32 KiB of fills per k = 128 and workgroup, against 1024 matrix-core
+// cycles) keeps the whole at 3.8 on the 70B d_proj slices (R = 4, T = 8192,
+// K = 7168, H = 8192: 1.02 ms). Four waves of 128 x 128, which read a third
+// less, and stages of half the length, fetched further ahead, were no faster.
+// Small calls are bound by the latency of the fills: about 128 KiB per compute
+// unit in flight.
 #include <atomic>
+#include <type_traits>
 
 #include "fc_launch.h"
 #include "fc_mxfp4.h"
@@ -38,9 +57,13 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int kFp4 = 4;                   // operand format of the f8f6f4 instructions
 constexpr int kStageBytes = 128;          // bytes of codes of a row in a stage
 constexpr int kStageScales = 8;           // bytes of scales
-constexpr int kStageK = 2 * kStageBytes;
+constexpr int kStageSteps = 4;
+constexpr int kScaleStages = 2;           // stages of one scale load
+constexpr int kScaleBytes = kScaleStages * kStageScales;
+constexpr int kSink = 1024;               // where the loads land that only keep the count
 constexpr int kGroupT = 4;                // token tiles per scheduling group
 constexpr int kXcds = 8;
+constexpr int kLdsBytes = 160 * 1024;     // LDS of a compute unit
 constexpr uint32_t kPast = 0xFFFFFFF0u;   // an offset past every resource
 // buffer resource word 3 for raw (untyped, unswizzled) 32-bit-addressed
 // buffers on gfx9-family GPUs
@@ -73,13 +96,6 @@ __device__ __forceinline__ void barrier_keep_loads() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int DT>
-__device__ __forceinline__ uint32_t round2(float a, float b) {
-    const f32x2 pair = {as_f32(a), as_f32(b)};
-    if constexpr (DT == 1) return __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, bf16x2));
-    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, f16x2));
-}
-
 struct MxArgs {
     const uint8_t *ac, *as, *wc, *ws;
     uint16_t *y;
@@ -91,20 +107,33 @@ struct MxArgs {
     int grid;
 };
 
-template <int DT, int BH, int BT, int WH, int WT, int NB, int EU>
-__global__ __launch_bounds__(WH *WT * 64) __attribute__((amdgpu_waves_per_eu(EU, EU)))
+template <int BH, int BT, int WH, int WT, int NB>
+struct Shape {
+    static constexpr int kRows = BH + BT;
+    static constexpr int kLds = NB * kRows * (kStageBytes + kScaleBytes) + kSink;
+    static constexpr int kPerCu = kLdsBytes / kLds > 2 ? 2 : kLdsBytes / kLds;
+    static_assert(kPerCu >= 1, "");
+};
+
+template <int DT, int BH, int BT, int WH, int WT, int NB, bool AHEAD>
+__global__ __launch_bounds__(WH *WT * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void matmul_mxfp4_kernel(const MxArgs p) {
     constexpr int NW = WH * WT;                    // waves
     constexpr int SH = BH / WH, ST = BT / WT;      // span of a wave
     constexpr int NH = SH / 32, NT = ST / 32;      // its blocks
     constexpr int BR = BH + BT;                    // rows of a stage: w, then a
     constexpr int RW = BR / NW;                    // rows that a wave stages
-    constexpr int kCodeLoads = RW / 8, kScaleLoads = RW / 32;
+    constexpr int kCodeLoads = RW / 8, kScaleLoads = RW >= 64 ? RW / 64 : 1;
     constexpr int kLoads = kCodeLoads + kScaleLoads;   // per wave and stage
-    constexpr int kCodes = BR * kStageBytes, kScales = BR * kStageScales;
-    static_assert(RW % 32 == 0 && BH % RW == 0, "a wave stages rows of one operand, whole instructions");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[NB * (kCodes + kScales)];
+    constexpr int kCodes = BR * kStageBytes, kScales = BR * kScaleBytes;
+    using S = Shape<BH, BT, WH, WT, NB>;
+    // with one wave per SIMD (LDS for one workgroup, 4 waves) the compiler keeps
+    // the accumulators in the other half of the registers
+    constexpr bool kAgprs = NW <= 4 && S::kPerCu == 1;
+    static_assert((RW == 32 || RW % 64 == 0) && BH % RW == 0, "a wave stages rows of one operand, whole instructions");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
     uint8_t *const lsc = lds + NB * kCodes;
+    uint8_t *const sink = lsc + NB * kScales;
 
     const uint32_t tid = __builtin_amdgcn_workitem_id_x();
     const uint32_t lane = tid & 63u;
@@ -158,14 +187,16 @@ void matmul_mxfp4_kernel(const MxArgs p) {
     };
     uint32_t lt = 0;          // tile and stage that the next loads fetch
     int ls = 0;
-    uint32_t lbuf = 0;
+    uint32_t lbuf = 0, lslot = 0;
     Tile cur;
     if (!tile_at(0, cur)) return;
     Source src = source_of(cur);
     const bool odd_k = p.code_row % kStageBytes != 0;
 
-    // Loads [from, to) of the cursor's stage. A code load covers 8 rows x 8
-    // chunks, a scale load 32 rows x 2 words. The whole offset is a lane's (the
+    // Loads [from, to) of the cursor's stage: a code load covers 8 rows x 8
+    // chunks, a scale load 64 rows (or the wave's 32). A stage that shares the
+    // scales of the one before loads nothing, into the sink, instead: the
+    // number of loads in flight stays fixed. The whole offset is a lane's (the
     // resource's bounds check covers it), recomputed for every call (`fresh`)
     // so that none of it is live across the epilogue.
     auto load_part = [&](int from, int to) {
@@ -173,26 +204,26 @@ void matmul_mxfp4_kernel(const MxArgs p) {
             const_cast<uint8_t *>(src.codes), (short)0, (int)src.code_bytes, kRawBufferFlags);
         const __amdgpu_buffer_rsrc_t sres = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<uint8_t *>(src.scales), (short)0, (int)src.scale_bytes, kRawBufferFlags);
-        const bool tail = odd_k && ls + 1 == p.stages;
         uint8_t *lc = lds + lbuf * kCodes + (uint32_t)wave * (RW * kStageBytes);
-        uint8_t *lw = lsc + lbuf * kScales + (uint32_t)wave * (RW * kStageScales);
+        const bool real = ls % kScaleStages == 0, tail = odd_k && ls + 1 == p.stages;
+        uint8_t *lw = real ? lsc + lslot * kScales + (uint32_t)wave * (RW * kScaleBytes) : sink;
         const uint32_t l = fresh(lane);
-        const uint32_t lrow = l >> 3, lpos = l & 7u;
+        const uint32_t ch = (l & 7u) ^ (l >> 4);      // the chunk of even loads; odd ones take ch ^ 4
+        const uint32_t co = (l >> 3) * p.code_row + (uint32_t)ls * kStageBytes;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             if (j < from || j >= to) continue;
             if (j < kCodeLoads) {
-                const uint32_t ch = lpos ^ ((4u * (j & 1) + (lrow >> 1)) & 7u);
-                uint32_t vo = (lrow + 8u * j) * p.code_row + (uint32_t)ls * kStageBytes + (ch << 4);
-                if (tail && ch >= 4u) vo = kPast;
+                const uint32_t c = ch ^ (4u * (j & 1));
+                const uint32_t vo = tail && c >= 4u ? kPast : co + 8u * j * p.code_row + (c << 4);
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     cres, (__attribute__((address_space(3))) void *)(lc + j * 1024), 16, vo, 0, 0, 0);
             } else {
                 const int i = j - kCodeLoads;
-                uint32_t vo = ((l >> 1) + 32u * i) * p.scale_row + (uint32_t)ls * kStageScales + (l & 1u) * 4u;
-                if (tail && (l & 1u)) vo = kPast;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    sres, (__attribute__((address_space(3))) void *)(lw + i * 256), 4, vo, 0, 0, 0);
+                const uint32_t vo = real ? (l + 64u * i) * p.scale_row + (uint32_t)ls * kStageScales : kPast;
+                if (RW >= 64 || l < RW)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                        sres, (__attribute__((address_space(3))) void *)(lw + (real ? i * 1024 : 0)), 16, vo, 0, 0, 0);
             }
         }
     };
@@ -200,7 +231,8 @@ void matmul_mxfp4_kernel(const MxArgs p) {
     // empty (the loads still count, and fill buffers that nobody reads)
     auto load_advance = [&]() {
         lbuf = lbuf + 1 == NB ? 0 : lbuf + 1;
-        if (++ls == p.stages) {
+        if (++ls == p.stages || ls % kScaleStages == 0) lslot = lslot + 1 == NB ? 0 : lslot + 1;
+        if (ls == p.stages) {
             ls = 0;
             Tile t;
             if (tile_at(++lt, t)) src = source_of(t);
@@ -212,39 +244,47 @@ void matmul_mxfp4_kernel(const MxArgs p) {
     // per-lane offsets within a stage, taken afresh for every tile so that none
     // of them is live across the epilogue
     struct Offs {
-        uint32_t ch[4];     // the row's chunk of step ks
-        uint32_t sc, sh;    // its scales, and the shift to this half's byte
+        uint32_t ch[kStageSteps];   // the row's chunk of step ks
+        uint32_t sc, sh;            // its scales, and the shift to this half's byte
     };
     auto offs = [&]() {
         const uint32_t l = fresh(lane);
         Offs o;
 #pragma unroll
-        for (uint32_t ks = 0; ks < 4; ++ks)
+        for (uint32_t ks = 0; ks < kStageSteps; ++ks)
             o.ch[ks] = (l & 31u) * kStageBytes + (((2u * ks + (l >> 5)) ^ ((l >> 1) & 7u)) << 4);
-        o.sc = (l & 31u) * kStageScales;
+        o.sc = (l & 31u) * kScaleBytes;
         o.sh = (l >> 5) * 8u;
         return o;
     };
-    uint32_t cbuf = 0;
-    u32x4 fw[2][NH], fa[2][NT];
-    uint32_t sw[2][NH], sa[2][NT];      // scale words of steps 0, 1 and of steps 2, 3
-    auto frag = [&](const Offs &o, uint32_t buf, int ks, int b) {
+    // fragments of a step and scale words of two, of every block
+    struct Frags {
+        u32x4 w[NH], a[NT];
+    };
+    struct Words {
+        uint32_t w[NH], a[NT];
+    };
+    auto frag = [&](Frags &f, const Offs &o, uint32_t buf, int ks, int b) {
         const uint8_t *st = lds + buf * kCodes;
-        if (b < NH) fw[ks & 1][b] = *reinterpret_cast<const u32x4 *>(st + (wh * SH + b * 32) * kStageBytes + o.ch[ks]);
-        if (b < NT) fa[ks & 1][b] = *reinterpret_cast<const u32x4 *>(st + (BH + wt * ST + b * 32) * kStageBytes + o.ch[ks]);
+        if (b < NH) f.w[b] = *reinterpret_cast<const u32x4 *>(st + (wh * SH + b * 32) * kStageBytes + o.ch[ks]);
+        if (b < NT) f.a[b] = *reinterpret_cast<const u32x4 *>(st + (BH + wt * ST + b * 32) * kStageBytes + o.ch[ks]);
     };
-    auto scale = [&](const Offs &o, uint32_t buf, int word, int b) {
-        const uint8_t *st = lsc + buf * kScales + word * 4;
-        if (b < NH) sw[word][b] = *reinterpret_cast<const uint32_t *>(st + (wh * SH + b * 32) * kStageScales + o.sc);
-        if (b < NT) sa[word][b] = *reinterpret_cast<const uint32_t *>(st + (BH + wt * ST + b * 32) * kStageScales + o.sc);
+    // word (0: steps 0 and 1) of stage q (of a scale load's two) in a slot, as read
+    auto words = [&](Words &r, const Offs &o, uint32_t slot, uint32_t q, int word, int b) {
+        const uint8_t *st = lsc + slot * kScales + q * kStageScales + word * 4;
+        if (b < NH) r.w[b] = *reinterpret_cast<const uint32_t *>(st + (wh * SH + b * 32) * kScaleBytes + o.sc);
+        if (b < NT) r.a[b] = *reinterpret_cast<const uint32_t *>(st + (BH + wt * ST + b * 32) * kScaleBytes + o.sc);
     };
-    auto shift = [&](const Offs &o, int word) {   // a step after the read
+    auto shifted = [&](const Words &r, const Offs &o, bool zero) {
+        Words c;
 #pragma unroll
-        for (int b = 0; b < NH; ++b) sw[word][b] >>= o.sh;
+        for (int b = 0; b < NH; ++b) c.w[b] = zero ? 0u : r.w[b] >> o.sh;
 #pragma unroll
-        for (int b = 0; b < NT; ++b) sa[word][b] >>= o.sh;
+        for (int b = 0; b < NT; ++b) c.a[b] = zero ? 0u : r.a[b] >> o.sh;
+        return c;
     };
     constexpr int NF = NH > NT ? NH : NT;
+    uint32_t cbuf = 0, cslot = 0;
 
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
@@ -253,11 +293,6 @@ void matmul_mxfp4_kernel(const MxArgs p) {
     }
     wait_loads<(NB - 1) * kLoads>();
     barrier_keep_loads();
-#pragma unroll
-    for (int b = 0; b < NF; ++b) {
-        frag(offs(), 0, 0, b);
-        scale(offs(), 0, 0, b);
-    }
 
     for (uint32_t it = 0;; ++it) {
         f32x16 acc[NH][NT];
@@ -265,59 +300,122 @@ void matmul_mxfp4_kernel(const MxArgs p) {
         for (int a = 0; a < NH; ++a)
 #pragma unroll
             for (int b = 0; b < NT; ++b) acc[a][b] = f32x16{};
-        auto step = [&](auto ks_, auto &&side) {
-            constexpr int ks = decltype(ks_)::value;
+        // The accumulators pass through here: without it the compiler gathers
+        // a stage's matrix instructions at its end, with all fragments live.
+        auto pin = [&](int nb) {
 #pragma unroll
-            for (int nb = 0; nb < NH; ++nb) {
-#pragma unroll
-                for (int tb = 0; tb < NT; ++tb)
-                    acc[nb][tb] = mfma_mx<(ks & 1) * 2>(fw[ks & 1][nb], fa[ks & 1][tb], acc[nb][tb],
-                                                        sw[ks >> 1][nb], sa[ks >> 1][tb]);
-                side(nb);
-                // the accumulators pass through here: without it the compiler
-                // gathers a stage's matrix instructions at its end, with all
-                // of its fragments live
-#pragma unroll
-                for (int tb = 0; tb < NT; ++tb) asm volatile("" : "+v"(acc[nb][tb]));
-                __builtin_amdgcn_sched_barrier(0);
+            for (int tb = 0; tb < NT; ++tb) {
+                if constexpr (kAgprs) asm volatile("" : "+a"(acc[nb][tb]));
+                else asm volatile("" : "+v"(acc[nb][tb]));
             }
         };
-        const Offs o = offs();
-        // fragment reads of a step's chunk nb, when a wave has more token than channel blocks the rest with the last
-        auto frags = [&](uint32_t buf, int ks, int nb) {
-            frag(o, buf, ks, nb);
-            if (nb == NH - 1)
-                for (int b = NH; b < NF; ++b) frag(o, buf, ks, b);
+        // row nb of a step's blocks
+        auto multiply = [&](auto odd_, int nb, const Frags &f, const Words &c) {
+#pragma unroll
+            for (int tb = 0; tb < NT; ++tb)
+                acc[nb][tb] = mfma_mx<decltype(odd_)::value * 2>(f.w[nb], f.a[tb], acc[nb][tb], c.w[nb], c.a[tb]);
         };
-        auto scales = [&](uint32_t buf, int word, int nb) {
-            scale(o, buf, word, nb);
-            if (nb == NH - 1)
-                for (int b = NH; b < NF; ++b) scale(o, buf, word, b);
+        constexpr std::integral_constant<int, 0> kEven;
+        constexpr std::integral_constant<int, 1> kOdd;
+        // from stage s to the next one of the stream
+        auto next_buf = [&]() { return cbuf + 1 == NB ? 0u : cbuf + 1; };
+        auto next_slot = [&](int s) {
+            const bool fresh_slot = s + 1 == p.stages || (s + 1) % kScaleStages == 0;
+            return !fresh_slot ? cslot : cslot + 1 == NB ? 0u : cslot + 1;
         };
-        for (int s = 0; s < p.stages; ++s) {
-            const uint32_t nbuf = cbuf + 1 == NB ? 0 : cbuf + 1;
-            shift(o, 0);
-            step(std::integral_constant<int, 0>{}, [&](int nb) {
-                frags(cbuf, 1, nb);
-                scales(cbuf, 1, nb);
-            });
-            step(std::integral_constant<int, 1>{}, [&](int nb) {
-                frags(cbuf, 2, nb);
-                if (nb == NH - 1) shift(o, 1);
-            });
-            step(std::integral_constant<int, 2>{}, [&](int nb) { frags(cbuf, 3, nb); });
-            // the next stage's loads are done (this wave's; the barrier makes
-            // them everybody's), and every wave has read this stage's last
-            // fragments: its buffer can be filled again
+        auto stage_of_slot = [&](int s) { return s == p.stages ? 0u : (uint32_t)s % kScaleStages; };
+        // the wait for the next stage's loads (this wave's; the barrier makes
+        // them everybody's); every wave has then also done its reads of this
+        // stage, whose buffer can be filled again
+        auto next_ready = [&]() {
             wait_loads<(NB - 2) * kLoads>();
             barrier_keep_loads();
-            step(std::integral_constant<int, 3>{}, [&](int nb) {
-                frags(nbuf, 0, nb);
-                scales(nbuf, 0, nb);
-                load_part(nb * kLoads / NH, (nb + 1) * kLoads / NH);
-            });
-            load_advance();
-            cbuf = nbuf;
+        };
+        const Offs o = offs();
+        if constexpr (AHEAD) {
+            struct Stage {
+                Frags f[kStageSteps];
+                Words r[2];
+            } st[2];
+            auto read = [&](Stage &x, uint32_t buf, uint32_t slot, uint32_t q) {
+#pragma unroll
+                for (int ks = 0; ks < kStageSteps; ++ks)
+#pragma unroll
+                    for (int b = 0; b < NF; ++b) {
+                        frag(x.f[ks], o, buf, ks, b);
+                        if (ks < 2) words(x.r[ks], o, slot, q, ks, b);
+                    }
+            };
+            auto body = [&](Stage &x, Stage &y, int s) {
+                next_ready();
+                const uint32_t nbuf = next_buf(), nslot = next_slot(s);
+                read(y, nbuf, nslot, stage_of_slot(s + 1));
+                load_part(0, kLoads);
+                load_advance();
+                const Words c0 = shifted(x.r[0], o, false), c1 = shifted(x.r[1], o, odd_k && s + 1 == p.stages);
+#pragma unroll
+                for (int nb = 0; nb < NH; ++nb) {
+                    multiply(kEven, nb, x.f[0], c0);
+                    multiply(kOdd, nb, x.f[1], c0);
+                    multiply(kEven, nb, x.f[2], c1);
+                    multiply(kOdd, nb, x.f[3], c1);
+                    pin(nb);
+                }
+                cbuf = nbuf;
+                cslot = nslot;
+            };
+            read(st[0], cbuf, cslot, 0);
+            int s = 0;
+            for (; s + 1 < p.stages; s += 2) {
+                body(st[0], st[1], s);
+                body(st[1], st[0], s + 1);
+            }
+            if (s < p.stages) body(st[0], st[1], s);
+        } else {
+            // the tile's first fragments (the last step before a tile's epilogue
+            // reads them too, but none is live across the epilogue)
+            Frags f[2];
+            Words r0, r1;
+#pragma unroll
+            for (int b = 0; b < NF; ++b) {
+                frag(f[0], o, cbuf, 0, b);
+                words(r0, o, cslot, 0, 0, b);
+            }
+            // step ks with `side`, the reads and loads that overlap it
+            auto step = [&](auto odd_, const Words &c, auto &&side) {
+#pragma unroll
+                for (int nb = 0; nb < NH; ++nb) {
+                    multiply(odd_, nb, f[decltype(odd_)::value], c);
+                    side(nb);
+                    if (nb == NH - 1)
+                        for (int b = NH; b < NF; ++b) side(b);
+                    pin(nb);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            auto load_share = [&](int part, int parts) {
+                if (part < parts) load_part(part * kLoads / parts, (part + 1) * kLoads / parts);
+            };
+            for (int s = 0; s < p.stages; ++s) {
+                const uint32_t nbuf = next_buf(), nslot = next_slot(s), nq = stage_of_slot(s + 1);
+                const Words c0 = shifted(r0, o, false);
+                step(kEven, c0, [&](int b) {
+                    frag(f[1], o, cbuf, 1, b);
+                    words(r1, o, cslot, stage_of_slot(s), 1, b);
+                });
+                step(kOdd, c0, [&](int b) { frag(f[0], o, cbuf, 2, b); });
+                const Words c1 = shifted(r1, o, odd_k && s + 1 == p.stages);
+                step(kEven, c1, [&](int b) { frag(f[1], o, cbuf, 3, b); });
+                next_ready();
+                step(kOdd, c1, [&](int b) {
+                    frag(f[0], o, nbuf, 0, b);
+                    words(r0, o, nslot, nq, 0, b);
+                    load_share(b, NH);
+                });
+                load_advance();
+                cbuf = nbuf;
+                cslot = nslot;
+            }
         }
 
         // epilogue: groups 2 q and 2 q + 1 of 4 channels, swapped between the
@@ -333,8 +431,8 @@ void matmul_mxfp4_kernel(const MxArgs p) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const f32x16 &v = acc[nb][tb];
-                    uint32_t a0 = round2<DT>(v[8 * q + 0], v[8 * q + 1]), a1 = round2<DT>(v[8 * q + 2], v[8 * q + 3]);
-                    uint32_t b0 = round2<DT>(v[8 * q + 4], v[8 * q + 5]), b1 = round2<DT>(v[8 * q + 6], v[8 * q + 7]);
+                    uint32_t a0 = mx_round2<DT>(v[8 * q + 0], v[8 * q + 1]), a1 = mx_round2<DT>(v[8 * q + 2], v[8 * q + 3]);
+                    uint32_t b0 = mx_round2<DT>(v[8 * q + 4], v[8 * q + 5]), b1 = mx_round2<DT>(v[8 * q + 6], v[8 * q + 7]);
                     const auto s0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
                     const auto s1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
                     const uint32_t w[4] = {(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
@@ -349,6 +447,7 @@ void matmul_mxfp4_kernel(const MxArgs p) {
                         }
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         if (!tile_at(it + 1, cur)) break;
@@ -372,8 +471,9 @@ int compute_units() {
     return n;
 }
 
-template <int DT, int BH, int BT, int WH, int WT, int NB, int EU>
-hipError_t launch_tiles(MxArgs p, int R, int per_cu, hipStream_t stream) {
+template <int DT, int BH, int BT, int WH, int WT, int NB, bool AHEAD>
+hipError_t launch_tiles(MxArgs p, int R, hipStream_t stream) {
+    constexpr int per_cu = Shape<BH, BT, WH, WT, NB>::kPerCu;
     p.tiles_t = (p.T + BT - 1) / BT;
     p.tiles_h = (p.H + BH - 1) / BH;
     const uint64_t total = (uint64_t)R * (uint64_t)p.tiles_t * (uint64_t)p.tiles_h;
@@ -382,18 +482,30 @@ hipError_t launch_tiles(MxArgs p, int R, int per_cu, hipStream_t stream) {
     if (total > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
     p.total = (uint32_t)total;
     p.grid = (int)(total < (uint64_t)cus * per_cu ? total : (uint64_t)cus * per_cu);
-    hipLaunchKernelGGL((matmul_mxfp4_kernel<DT, BH, BT, WH, WT, NB, EU>), dim3((unsigned)p.grid),
+    hipLaunchKernelGGL((matmul_mxfp4_kernel<DT, BH, BT, WH, WT, NB, AHEAD>), dim3((unsigned)p.grid),
                        dim3(WH * WT * 64), 0, stream, p);
     return hipGetLastError();
 }
 
+// The largest tile whose tiles occupy at least three quarters of the compute
+// units; 64 x 64 where none does, and for at most 64 tokens. Larger tiles move
+// fewer bytes per product, smaller ones spread over more units. Measured, us
+// with tiles of 64 / 128 / 256 (bf16; R, T, K, H):
+//   1, 2048, 2048, 2048: 15.5 / 12.6 / 19.8     1, 512, 4096, 4096: 14.5 / 16.6 / 29.8
+//   4, 768, 3584, 4096: 55 / 40 / 34            2, 384, 4096, 4096: 19.5 / 17.6 / 30.1
+//   4, 128, 2048, 8192: 16.3 / 14.5 / 20.1      4, 8192, 7168, 8192: 2133 / 1392 / 1025
+// At most one tile per unit leaves the LDS for twice the stages (8 against 4:
+// 1, 256, 4096, 4096 11.6 against 12.1).
 template <int DT>
 hipError_t by_shape(const MxArgs &p, int R, hipStream_t stream) {
     const int cus = compute_units();
+    if (cus <= 0) return hipErrorInvalidDevice;
     auto tiles = [&](int b) { return (uint64_t)R * (uint64_t)((p.T + b - 1) / b) * (uint64_t)((p.H + b - 1) / b); };
-    if (tiles(256) >= (uint64_t)cus) return launch_tiles<DT, 256, 256, 2, 4, 2, 2>(p, R, 1, stream);
-    if (tiles(128) >= (uint64_t)cus) return launch_tiles<DT, 128, 128, 2, 2, 4, 1>(p, R, 1, stream);
-    return launch_tiles<DT, 64, 64, 2, 2, 4, 2>(p, R, 2, stream);
+    const uint64_t full = (uint64_t)cus * 3 / 4;
+    if (p.T > 64 && tiles(256) >= full) return launch_tiles<DT, 256, 256, 2, 4, 2, false>(p, R, stream);
+    if (p.T > 64 && tiles(128) >= full) return launch_tiles<DT, 128, 128, 2, 2, 4, false>(p, R, stream);
+    if (tiles(64) <= (uint64_t)cus) return launch_tiles<DT, 64, 64, 2, 2, 8, true>(p, R, stream);
+    return launch_tiles<DT, 64, 64, 2, 2, 4, true>(p, R, stream);
 }
 
 }  // namespace
@@ -401,6 +513,8 @@ hipError_t by_shape(const MxArgs &p, int R, hipStream_t stream) {
 hipError_t launch_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                const uint8_t *w_codes, const uint8_t *w_scales, int R, int T, int Kp,
                                int H, int dtype, uint16_t *y, hipStream_t stream) {
+    if (T <= kMxFewTokens && (uint64_t)R * (uint64_t)H < kMxFewChannels)
+        return launch_matmul_mxfp4_few(a_codes, a_scales, w_codes, w_scales, R, T, Kp, H, dtype, y, stream);
     MxArgs p = {};
     p.ac = a_codes;
     p.as = a_scales;
@@ -409,7 +523,7 @@ hipError_t launch_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
     p.y = y;
     p.T = T;
     p.H = H;
-    p.stages = (Kp + kStageK - 1) / kStageK;
+    p.stages = (Kp / kMxStepElems + 1) / 2;
     p.code_row = (uint32_t)Kp / 2;
     p.scale_row = (uint32_t)Kp / kMxBlockElems;
     return dtype == 0 ? by_shape<0>(p, R, stream) : by_shape<1>(p, R, stream);

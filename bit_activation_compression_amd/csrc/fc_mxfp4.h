@@ -67,4 +67,31 @@ __device__ __forceinline__ uint32_t mx_encode8(const u32x4 &v, float scale) {
     return q;
 }
 
+// 8 values from element e of a row of K, zeros past its end.
+__device__ __forceinline__ u32x4 mx_load8(const uint16_t *row, uint32_t e, uint32_t K) {
+    if (e + kLaneElems <= K) return *reinterpret_cast<const u32x4_u16 *>(row + e);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (uint32_t k = 0; k < kLaneElems; ++k)
+        if (e + k < K) w[k / 2] |= (uint32_t)row[e + k] << (16 * (k & 1));
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
+// The scale byte of the block that 4 neighbouring lanes hold, 8 values each.
+template <int DT>
+__device__ __forceinline__ uint32_t mx_block_scale(const u32x4 &v) {
+    uint32_t m = abs_max8(v);
+    m = pk_max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+    m = pk_max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));   // lane ^ 2
+    return mx_scale_byte<DT>((m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16));
+}
+
+// Two binary32 sums rounded to the dtype, the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t mx_round2(float a, float b) {
+    const f32x2 pair = {as_f32(a), as_f32(b)};
+    if constexpr (DT == 1) return __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, bf16x2));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, f16x2));
+}
+
 }  // namespace fc

@@ -18,16 +18,6 @@ namespace {
 
 constexpr int kUnits = 2;   // units per lane
 
-// 8 values from element e of a row of K, zeros past its end.
-__device__ __forceinline__ u32x4 load8(const uint16_t *row, uint32_t e, uint32_t K) {
-    if (e + kLaneElems <= K) return *reinterpret_cast<const u32x4_u16 *>(row + e);
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (uint32_t k = 0; k < kLaneElems; ++k)
-        if (e + k < K) w[k / 2] |= (uint32_t)row[e + k] << (16 * (k & 1));
-    return u32x4{w[0], w[1], w[2], w[3]};
-}
-
 // Row and column of a unit: the workgroup's first unit by one 64-bit division
 // of uniform values, the lane's from there.
 struct Place {
@@ -63,18 +53,14 @@ __global__ __launch_bounds__(kBlockThreads) void quantize_mxfp4_kernel(
                 v[u] = *reinterpret_cast<const u32x4 *>(x + (base + off) * kLaneElems);
             } else {
                 const Place p = place(row0, unit0, off, (uint32_t)per_row);
-                v[u] = load8(x + p.row * (uint64_t)K, p.col, (uint32_t)K);
+                v[u] = mx_load8(x + p.row * (uint64_t)K, p.col, (uint32_t)K);
             }
         }
     }
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
         const uint32_t off = u * kBlockThreads + tid;
-        uint32_t m = abs_max8(v[u]);
-        m = pk_max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, true));
-        m = pk_max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, true));
-        const uint32_t top = (m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16);
-        const uint32_t byte = mx_scale_byte<DT>(top);
+        const uint32_t byte = mx_block_scale<DT>(v[u]);
         uint32_t q = mx_encode8<DT>(v[u], mx_scale(byte));
         if (byte == 255u) q = 0;
         if (base + off < units) {
