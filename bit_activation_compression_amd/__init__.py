@@ -440,14 +440,14 @@ def _launch(name: str, device, stream, *args) -> None:
         raise FcError(st, name)
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor for a call on `stream` (None: torch's current one). It belongs to
-    that stream: memory that other streams still use cannot come back in it, and it is
-    not handed on before the call's work is done."""
+def _empty(like: torch.Tensor, shape, dtype, stream):
+    """A new tensor on like's device for a call on `stream` (None: torch's current one).
+    It belongs to that stream: memory that other streams still use cannot come back in
+    it, and it is not handed on before the call's work is done."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _like(t: torch.Tensor, name: str, shape: tuple, dtype, device) -> int:
@@ -480,13 +480,13 @@ def _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, strea
     else:
         gate_tokens = 1
     if h is None:
-        h = torch.empty_like(residual) if stream is None else _empty(rows, dt, dev, stream)
+        h = torch.empty_like(residual) if stream is None else _empty(residual, rows, dt, stream)
         ph = h.data_ptr()
     else:
         ph = _like(h, "h", rows, dt, dev)
     if w_pre is not None:
         if y is None:
-            y = torch.empty_like(residual) if stream is None else _empty(rows, dt, dev, stream)
+            y = torch.empty_like(residual) if stream is None else _empty(residual, rows, dt, stream)
             py = y.data_ptr()
         else:
             py = _like(y, "y", rows, dt, dev)
@@ -547,7 +547,7 @@ def fc_allreduce_emulated_norm(x: torch.Tensor, bits: int, group: int, residual:
     code, pr, pw, pg, gate_tokens, pv, ph, py, h, y = _norm_operands(
         T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
     if workspace is None:
-        workspace = _empty(max(fc_workspace_bytes(R, T, H, bits, group, bits2), 1), torch.uint8, dev, stream)
+        workspace = _empty(x, max(fc_workspace_bytes(R, T, H, bits, group, bits2), 1), torch.uint8, stream)
     _room(workspace, "workspace", 0, dev)
     _launch("fc_allreduce_emulated_norm", dev, stream, x.data_ptr(), code, R, T, H, bits, bits2, group, pr, pw, pg,
             gate_tokens, pv, res_scale, out_scale, eps, ph, py, workspace.data_ptr(),
@@ -586,12 +586,12 @@ def fc_quantize_mxfp4(x: torch.Tensor, codes=None, scales=None, stream=None):
     R, T, K = _rows3(x, "x")
     dev, Kp, lead = x.device, _mx_padded(K), x.shape[:-1]
     if codes is None:
-        codes = _empty((*lead, Kp // 2), torch.uint8, dev, stream)
+        codes = _empty(x, (*lead, Kp // 2), torch.uint8, stream)
         pc = codes.data_ptr()
     else:
         pc = _like(codes, "codes", (*lead, Kp // 2), torch.uint8, dev)
     if scales is None:
-        scales = _empty((*lead, Kp // 32), torch.uint8, dev, stream)
+        scales = _empty(x, (*lead, Kp // 32), torch.uint8, stream)
         ps = scales.data_ptr()
     else:
         ps = _like(scales, "scales", (*lead, Kp // 32), torch.uint8, dev)
@@ -607,7 +607,7 @@ def fc_dequantize_mxfp4(codes, scales, K: int, dtype: torch.dtype, out=None, str
         raise ValueError(f"codes hold rows of {Kp} values, K is {K}")
     shape = (*codes.shape[:-1], K)
     if out is None:
-        out = _empty(shape, dtype, dev, stream)
+        out = _empty(codes, shape, dtype, stream)
         po = out.data_ptr()
     else:
         po = _like(out, "out", shape, dtype, dev)
@@ -625,7 +625,7 @@ def fc_matmul_mxfp4(a_codes, a_scales, w_codes, w_scales, dtype: torch.dtype, y=
         raise ValueError("a must be [R, T, K] and w [R, H, K]")
     shape = (*a_codes.shape[:-1], H)
     if y is None:
-        y = _empty(shape, dtype, dev, stream)
+        y = _empty(a_codes, shape, dtype, stream)
         py = y.data_ptr()
     else:
         py = _like(y, "y", shape, dtype, dev)
@@ -648,7 +648,7 @@ def fc_linear_mxfp4(a: torch.Tensor, w_codes, w_scales, y=None, workspace=None, 
         raise ValueError("a must be [R, T, K] and w [R, H, K]")
     shape = (*a.shape[:-1], H)
     if y is None:
-        y = _empty(shape, a.dtype, dev, stream)
+        y = _empty(a, shape, a.dtype, stream)
         py = y.data_ptr()
     else:
         py = _like(y, "y", shape, a.dtype, dev)
@@ -656,7 +656,7 @@ def fc_linear_mxfp4(a: torch.Tensor, w_codes, w_scales, y=None, workspace=None, 
     if workspace is None:
         need = fc_linear_mxfp4_workspace_bytes(R, T, K)
         if need:
-            workspace = _empty(need, torch.uint8, dev, stream)
+            workspace = _empty(a, need, torch.uint8, stream)
             have, pk = need, workspace.data_ptr()
     else:
         _room(workspace, "workspace", 0, dev)

@@ -375,10 +375,18 @@ fc_status fc_allreduce_emulated_norm(const void *x, fc_dtype dt, int R, int T, i
     uint16_t *s2 = reinterpret_cast<uint16_t *>(wb + L.off[4]);
     uint16_t *z2 = reinterpret_cast<uint16_t *>(wb + L.off[5]);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    st = from_hip(run_quantize(x, dt, n * (uint64_t)R, bits1, group, wb, s1, z1, s));
-    if (st != FC_OK) return st;
-    st = from_hip(run_dsr(wb, s1, z1, R, n, bits1, bits2, group, g2, codes2, s2, z2, s));
-    if (st != FC_OK) return st;
+    if (fc::allreduce_small_applies(R, n, group, g2)) {
+        // launch-bound shapes: both payloads in one launch
+        st = from_hip(fc::launch_allreduce_small(static_cast<const uint16_t *>(x), (int)dt, R, n, bits1,
+                                                 bits2, group, wb, s1, z1, codes2, s2, z2, nullptr,
+                                                 nullptr, s));
+        if (st != FC_OK) return st;
+    } else {
+        st = from_hip(run_quantize(x, dt, n * (uint64_t)R, bits1, group, wb, s1, z1, s));
+        if (st != FC_OK) return st;
+        st = from_hip(run_dsr(wb, s1, z1, R, n, bits1, bits2, group, g2, codes2, s2, z2, s));
+        if (st != FC_OK) return st;
+    }
     return from_hip(run_dequantize_norm(norm_args(T, H, residual, w_post, gate, gate_tokens, w_pre,
                                                   res_scale, out_scale, eps, h, y),
                                         codes2, s2, z2, bits2, g2, dt, s));

@@ -43,7 +43,8 @@ hipError_t launch_linear_quantize(const uint16_t *a, const uint16_t *w, int dtyp
 // stage-1 payload (codes1, s1, z1 as launch_quantize writes them), stage-2
 // payload (as launch_dequant_sum_requant writes them) and the output (as
 // launch_dequantize or, with residual != NULL, launch_dequantize_residual
-// writes it), identical bit for bit. Applies when allreduce_small_applies.
+// writes it), identical bit for bit; with out == NULL the payloads only.
+// Applies when allreduce_small_applies.
 constexpr uint64_t kAllreduceSmallMaxElems = uint64_t(1) << 24;   // R * T * H
 bool allreduce_small_applies(int R, uint64_t n, int group, int group2);
 hipError_t launch_allreduce_small(const uint16_t *x, int dtype, int R, uint64_t n, int bits1,

@@ -9,7 +9,10 @@
 // the one to E2M1.
 //
 // Units of 8 values are numbered over the padded rows (Kp / 8 each); rows
-// that need no padding are one flat run.
+// that need no padding are one flat run, and its 16-bit values are loaded and
+// stored non-temporally: 8192 x 8192 bf16 quantized and dequantized in 51.9 us
+// (6.5 TB/s) against 58.1 through the caches; 1, 2 and 4 units per lane 58.2 /
+// 58.1 / 59.5. Rows of 8191, which are aligned to 2 bytes only, take 69.
 #include "fc_launch.h"
 #include "fc_mxfp4.h"
 
@@ -50,7 +53,7 @@ __global__ __launch_bounds__(kBlockThreads) void quantize_mxfp4_kernel(
         v[u] = u32x4{0, 0, 0, 0};
         if (base + off < units) {
             if constexpr (FLAT) {
-                v[u] = *reinterpret_cast<const u32x4 *>(x + (base + off) * kLaneElems);
+                v[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x + (base + off) * kLaneElems));
             } else {
                 const Place p = place(row0, unit0, off, (uint32_t)per_row);
                 v[u] = mx_load8(x + p.row * (uint64_t)K, p.col, (uint32_t)K);
@@ -109,7 +112,7 @@ __global__ __launch_bounds__(kBlockThreads) void dequantize_mxfp4_kernel(
         constexpr uint32_t kNan = DT == 1 ? 0x7FC07FC0u : 0x7E007E00u;
         if (byte[u] == 255u) w = u32x4{kNan, kNan, kNan, kNan};
         if constexpr (FLAT) {
-            *reinterpret_cast<u32x4 *>(out + (base + off) * kLaneElems) = w;
+            __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(out + (base + off) * kLaneElems));
         } else {
             const Place p = place(row0, unit0, off, (uint32_t)per_row);
             uint16_t *row = out + p.row * (uint64_t)K;
