@@ -226,7 +226,7 @@ hipError_t launch(FewArgs p, int R, hipStream_t stream) {
     constexpr int group = kWaves / SPLIT * 16;
     p.groups = (p.H + group - 1) / group;
     const uint64_t blocks = (uint64_t)R * (uint64_t)p.groups;
-    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    if (blocks * (kWaves * kWave) > 0xFFFFFFFFull) return hipErrorInvalidConfiguration;
     const size_t quant = QUANT ? (size_t)p.T * ((size_t)p.steps * (kStepBytes + kStepScales) + kLdsPad) : 0;
     const size_t parts = SPLIT > 1 ? (size_t)(SPLIT - 1) * NT * kWave * sizeof(f32x4) : 0;
     hipLaunchKernelGGL((matmul_mxfp4_few_kernel<DT, NT, CH, SPLIT, QUANT>), dim3((unsigned)blocks),

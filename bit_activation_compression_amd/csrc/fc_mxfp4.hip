@@ -39,7 +39,7 @@ __global__ __launch_bounds__(kBlockThreads) void quantize_mxfp4_kernel(
     const uint16_t *__restrict__ x, uint64_t units, int K, int per_row, uint8_t *__restrict__ codes,
     uint8_t *__restrict__ scales) {
     const uint32_t tid = __builtin_amdgcn_workitem_id_x();
-    const uint64_t base = (uint64_t)__builtin_amdgcn_workgroup_id_x() * (kBlockThreads * kUnits);
+    const uint64_t base = grid_index() * (kBlockThreads * kUnits);
     uint64_t row0 = 0;
     uint32_t unit0 = 0;
     if constexpr (!FLAT) {
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(kBlockThreads) void dequantize_mxfp4_kernel(
     const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, uint64_t units, int K,
     int per_row, uint16_t *__restrict__ out) {
     const uint32_t tid = __builtin_amdgcn_workitem_id_x();
-    const uint64_t base = (uint64_t)__builtin_amdgcn_workgroup_id_x() * (kBlockThreads * kUnits);
+    const uint64_t base = grid_index() * (kBlockThreads * kUnits);
     uint64_t row0 = 0;
     uint32_t unit0 = 0;
     if constexpr (!FLAT) {
@@ -128,10 +128,11 @@ __global__ __launch_bounds__(kBlockThreads) void dequantize_mxfp4_kernel(
     }
 }
 
-bool grid_of(uint64_t units, unsigned *blocks) {
+// Workgroups (a grid has at most 2^16 rows of them: 2^45 values).
+bool grid_of(uint64_t units, dim3 *grid) {
     const uint64_t n = (units + kBlockThreads * kUnits - 1) / (kBlockThreads * kUnits);
-    *blocks = (unsigned)n;
-    return n <= 0x7FFFFFFFull;
+    *grid = grid_of_blocks(n);
+    return n <= uint64_t(65535) << kGridRow;
 }
 
 }  // namespace
@@ -140,10 +141,10 @@ hipError_t launch_quantize_mxfp4(const uint16_t *x, int dtype, uint64_t rows, in
                                  uint8_t *codes, uint8_t *scales, hipStream_t stream) {
     const int per_row = Kp / kLaneElems;
     const uint64_t units = rows * (uint64_t)per_row;
-    unsigned blocks;
-    if (!grid_of(units, &blocks)) return hipErrorInvalidConfiguration;
+    dim3 grid;
+    if (!grid_of(units, &grid)) return hipErrorInvalidConfiguration;
 #define FC_GO(DT, FLAT)                                                                              \
-    hipLaunchKernelGGL((quantize_mxfp4_kernel<DT, FLAT>), dim3(blocks), dim3(kBlockThreads), 0, stream, x, \
+    hipLaunchKernelGGL((quantize_mxfp4_kernel<DT, FLAT>), grid, dim3(kBlockThreads), 0, stream, x, \
                        units, K, per_row, codes, scales)
     if (dtype == 0) {
         if (K == Kp) FC_GO(0, true);
@@ -160,10 +161,10 @@ hipError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, 
                                    int Kp, int dtype, uint16_t *out, hipStream_t stream) {
     const int per_row = Kp / kLaneElems;
     const uint64_t units = rows * (uint64_t)per_row;
-    unsigned blocks;
-    if (!grid_of(units, &blocks)) return hipErrorInvalidConfiguration;
+    dim3 grid;
+    if (!grid_of(units, &grid)) return hipErrorInvalidConfiguration;
 #define FC_GO(DT, FLAT)                                                                            \
-    hipLaunchKernelGGL((dequantize_mxfp4_kernel<DT, FLAT>), dim3(blocks), dim3(kBlockThreads), 0, stream, \
+    hipLaunchKernelGGL((dequantize_mxfp4_kernel<DT, FLAT>), grid, dim3(kBlockThreads), 0, stream, \
                        codes, scales, units, K, per_row, out)
     if (dtype == 0) {
         if (K == Kp) FC_GO(0, true);

@@ -121,7 +121,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormArgs a) {
     __shared__ float part[2][kNormThreads / kWave];
     const int NT = a.waves * kWave;
     const int tid = (int)__builtin_amdgcn_workitem_id_x();
-    const uint64_t row = __builtin_amdgcn_workgroup_id_x();
+    const uint64_t row = grid_index();
+    if (row >= (uint64_t)a.T) return;
     const int H = a.H;
     // Vector v of the thread: its elements are those from elem(v), if any. All
     // loads take 8 whole ones, from begin(v): the row's last 8 where fewer (or
@@ -287,7 +288,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormArgs a) {
 template <int DT, int SRC, bool GEN, int V>
 hipError_t launch_norm_rows(NormArgs a, int nv, hipStream_t stream) {
     a.waves = (nv + V * kWave - 1) / (V * kWave);
-    hipLaunchKernelGGL((norm_kernel<DT, SRC, GEN, V>), dim3((unsigned)a.T), dim3((unsigned)(a.waves * kWave)),
+    hipLaunchKernelGGL((norm_kernel<DT, SRC, GEN, V>), grid_of_blocks((uint64_t)a.T), dim3((unsigned)(a.waves * kWave)),
                        0, stream, a);
     return hipGetLastError();
 }

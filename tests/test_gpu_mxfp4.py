@@ -132,6 +132,13 @@ PRODUCTS = [(1, 1, 128, 16), (1, 1, 32, 1), (2, 1, 2048, 512), (1, 2, 100, 7), (
             (8, 3, 256, 2050), (1, 700, 96, 5)]
 
 
+# enough tiles for the 128 and the 256 tile, and for several tiles per workgroup; K an even and an odd
+# multiple of 128, shorter and longer than the stages in flight
+PRODUCTS += [(4, 520, 256, 1300), (3, 1000, 384, 1160), (8, 600, 1408, 650), (2, 2300, 128, 1700),
+             (8, 1300, 384, 1030), (8, 1300, 256, 2100), (4, 2050, 640, 1800), (1, 4000, 128, 3500), (2, 3000, 1408, 2100),
+             (4, 100, 384, 4100), (4, 3, 2048, 4100), (2, 16, 1000, 8200)]
+
+
 def _operands(R, T, K, H, seed, spread):
     g = torch.Generator().manual_seed(seed)
     Kp = -(-K // 128) * 128
@@ -307,6 +314,61 @@ def test_other_stream_and_graph_replays():
             fc.fc_linear_mxfp4(a, wc, ws, y, work[1])     # beside the replay, with a workspace of its own
             torch.cuda.synchronize()
             assert torch.equal(y, y2), f"T={T} replay {i}"
+
+
+def test_more_rows_than_a_grid_row():
+    """A grid row of 2^20 workgroups of 512 units of 8 values: rows of 128 (whole) and of 100 (padded)."""
+    for K, rows in ((128, (1 << 25) + 70), (100, (1 << 25) + 70)):
+        _say(f"quantize {rows} x {K}")
+        g = torch.Generator(device="cuda").manual_seed(K)
+        x = torch.randn((rows, K), generator=g, device="cuda", dtype=BF16)
+        codes, scales = fc.fc_quantize_mxfp4(x)
+        out = fc.fc_dequantize_mxfp4(codes, scales, K, BF16)
+        torch.cuda.synchronize()
+        at = torch.tensor([0, 1, (1 << 25) - 33, (1 << 25) - 1, 1 << 25, (1 << 25) + 32, rows - 1])
+        want = ref.mx_quantize(x[at].cpu().double())
+        assert torch.equal(codes[at].cpu(), want[0]) and torch.equal(scales[at].cpu(), want[1])
+        assert torch.equal(out[at].cpu(), ref.mx_dequantize(*want, K).to(BF16))
+        del x, codes, scales, out
+
+
+def test_block_chain_captured():
+    """The chain below in a graph, with eager work between the replays."""
+    R, T, K, H = 4, 24, 512, 1024
+    a = torch.randn((R, T, K), device="cuda").to(BF16)
+    wc, ws = fc.fc_quantize_mxfp4(torch.randn((R, H, K), device="cuda").mul_(K ** -0.5).to(BF16))
+    vc, vs = fc.fc_quantize_mxfp4(torch.randn((512, H), device="cuda").mul_(H ** -0.5).to(BF16))
+    res = torch.randn((T, H), device="cuda").to(BF16)
+    w = torch.ones(H, device="cuda", dtype=BF16)
+
+    def buffers():
+        e = lambda *s: torch.empty(s, dtype=BF16, device="cuda")
+        b = lambda n: torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+        return (e(R, T, H), e(T, H), e(T, H), e(T, 512), b(fc.fc_linear_mxfp4_workspace_bytes(R, T, K)),
+                b(fc.fc_workspace_bytes(R, T, H, 4, 128)), b(fc.fc_linear_mxfp4_workspace_bytes(1, T, H)))
+
+    def chain(y, h, n, out, w1, w2, w3):
+        fc.fc_linear_mxfp4(a, wc, ws, y, w1)
+        fc.fc_allreduce_emulated_norm(y, 4, 128, res, w_post=w, w_pre=w, h=h, y=n, workspace=w2)
+        fc.fc_linear_mxfp4(n, vc, vs, out, w3)
+
+    eager, captured = buffers(), buffers()
+    chain(*eager)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(*captured)
+    torch.cuda.synchronize()
+    for i in range(4):
+        a.copy_(torch.randn((R, T, K), device="cuda"))
+        for v in captured[:4]:
+            v.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        chain(*eager)
+        torch.cuda.synchronize()
+        for e, c in zip(eager[:4], captured[:4]):
+            assert torch.equal(e, c), f"replay {i}"
 
 
 def test_block_chain():

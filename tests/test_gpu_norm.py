@@ -287,3 +287,36 @@ def test_other_stream_and_graph_replays():
         fc.fc_allreduce_emulated_norm(x, 4, 128, **d, gate_tokens=T, h=h, y=y, workspace=ws)
         torch.cuda.synchronize()
         assert torch.equal(h, h2) and torch.equal(y, y2), f"replay {i}"
+
+
+def _sampled(T, H, rows, dt, gate_tokens=1):
+    """Inputs made on the GPU and the 64-bit check of some rows of the outputs."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn((T, H), generator=g, device="cuda").to(dt)
+    res = torch.randn((T, H), generator=g, device="cuda").to(dt)
+    w = (1 + 0.2 * torch.randn(H, generator=g, device="cuda")).to(dt)
+    h, y = fc.fc_residual_norm(x, res, w_post=w, w_pre=w, eps=EPS)
+    torch.cuda.synchronize()
+    at = torch.tensor(rows)
+    d = dict(x=x[at].cpu().double(), residual=res[at].cpu().double(), w_post=w.cpu().double(), gate=None, w_pre=w.cpu().double())
+    _check(h[at], y[at], d, 1, dt, 1.0, 1.0)
+    return x, res, w, h, y
+
+
+def test_outputs_past_the_cache():
+    """Outputs of more than 256 MiB are stored past it; the rows are the same as one by one."""
+    T, H = 8200, 8192
+    _say("norm past the cache")
+    rows = [0, 1, 4095, 8191, 8199]
+    x, res, w, h, y = _sampled(T, H, rows, BF16)
+    for r in rows:
+        h1, y1 = fc.fc_residual_norm(x[r:r + 1], res[r:r + 1], w_post=w, w_pre=w, eps=EPS)
+        # one vector per thread against two: other sums, so within a rounding of each other
+        assert (h1 - h[r:r + 1]).abs().max() <= 2.0 ** -7 * h1.abs().max()
+
+
+def test_more_rows_than_a_grid_row():
+    T = (1 << 20) + 5
+    _say("norm 2^20 + 5 rows")
+    _sampled(T, 8, [0, 1, (1 << 20) - 1, 1 << 20, T - 1], F16)
+    _sampled(T, 20, [3, (1 << 20) - 1, 1 << 20, T - 1], BF16)

@@ -151,6 +151,53 @@ def test_linear_workspace_holds_codes_and_scales():
         assert fc.fc_linear_mxfp4_workspace_bytes(*bad) == 0
 
 
+def test_checks_under_sanitizers_match_the_library(tmp_path):
+    """The checks' own code, built with address and undefined-behaviour sanitizers."""
+    import shutil
+    import subprocess
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not available")
+    exe = str(tmp_path / "driver")
+    r = subprocess.run(["g++", "-fsanitize=address,undefined", "-fno-sanitize-recover=all", "-O1", "-g", "-std=c++17",
+                        f"-I{os.path.join(ROOT, 'include')}", f"-I{os.path.join(ROOT, 'bit_activation_compression_amd', 'csrc')}",
+                        os.path.join(ROOT, "tests", "sanitize", "validate_layer_driver.cpp"), "-o", exe],
+                       capture_output=True, text=True)
+    if r.returncode != 0 and "sanitize" in r.stderr:
+        pytest.skip("sanitizer runtime not available")
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "runtime error" not in r.stderr and "Sanitizer" not in r.stderr, r.stderr[-2000:]
+    values = [0.0, 1.0, -2.0, 1e-39, 1e30, INF, -INF, NAN]
+    refused = accepted = 0
+    for line in r.stdout.splitlines():
+        head, tail = line.split(" : ")
+        kind, *args = head.split()
+        args, got = [int(v) for v in args], [int(v) for v in tail.split()]
+        if kind == "norm":
+            T, H, gt, v, bad = args
+            x = None if bad == 1 else P(0)
+            h = x if bad == 2 else P(5, 8 if bad == 3 else 0)
+            y = None if bad == 4 else P(6)
+            res = h if bad == 5 else P(1)
+            for st, kw in ((got[0], dict(out_scale=values[v])), (got[1], dict(eps=values[v]))):
+                if st == 0 and T > 0:
+                    accepted += 1          # not called: the pointers are made up
+                    continue
+                refused += st != 0
+                assert _norm(x=x, residual=res, dt=1, T=T, H=H, w_post=P(2), gate=P(3), gate_tokens=gt, w_pre=P(4),
+                             h=h, y=y, **kw) == st, line
+        else:
+            R, T, K, H = args
+            if got[0] != 0:
+                refused += 1
+                assert fc.lib().fc_quantize_mxfp4(P(0), 1, R, T, K, P(1), P(2), None) == got[0], line
+            if got[1] != 0:
+                refused += 1
+                assert fc.lib().fc_matmul_mxfp4(P(0), P(1), P(2), P(3), R, T, K, H, 1, P(4), None) == got[1], line
+            assert got[2] == -(-K // 128) * 128 and got[3] == got[2] // 2
+    assert refused > 1000 and accepted > 100
+
+
 # --- the 64-bit statements ---------------------------------------------------
 
 def test_reference_quantizer_on_the_grid_ties_and_limits():
