@@ -60,19 +60,6 @@ __device__ __forceinline__ uint64_t wave_index() {
     return (uint64_t)__builtin_amdgcn_workgroup_id_x() * kWavesPerBlock + w;
 }
 
-// A launch counts its threads along x in 32 bits, so the workgroups of kernels
-// with one workgroup for little data lie in rows of 2^20 (x) along y.
-constexpr int kGridRow = 20;
-
-__device__ __forceinline__ uint64_t grid_index() {
-    return (uint64_t)__builtin_amdgcn_workgroup_id_y() << kGridRow | __builtin_amdgcn_workgroup_id_x();
-}
-
-inline dim3 grid_of_blocks(uint64_t blocks) {
-    const uint64_t row = uint64_t(1) << kGridRow;
-    return blocks <= row ? dim3((unsigned)blocks) : dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
-}
-
 // Hides a value from the optimizer (no instruction is emitted).
 __device__ __forceinline__ uint32_t opaque(uint32_t v) {
     asm("" : "+v"(v));

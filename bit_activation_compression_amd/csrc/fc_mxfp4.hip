@@ -13,6 +13,7 @@
 // stored non-temporally: 8192 x 8192 bf16 quantized and dequantized in 51.9 us
 // (6.5 TB/s) against 58.1 through the caches; 1, 2 and 4 units per lane 58.2 /
 // 58.1 / 59.5. Rows of 8191, which are aligned to 2 bytes only, take 69.
+#include "fc_grid.h"
 #include "fc_launch.h"
 #include "fc_mxfp4.h"
 
