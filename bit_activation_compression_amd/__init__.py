@@ -421,11 +421,23 @@ def workspace_views(workspace: torch.Tensor, R: int, T: int, H: int, bits: int, 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+_INT_MAX = 2**31 - 1
+
+
+def _ints(**values) -> None:
+    """The library takes 32-bit integers, and ctypes would cut longer ones down to them."""
+    for name, v in values.items():
+        if not -_INT_MAX <= v <= _INT_MAX:
+            raise ValueError(f"{name} must fit 32 bits, not {v}")
+
+
 def _launch(name: str, device, stream, *args) -> None:
     """Calls the library on `device` (it launches on the current one) and `stream`."""
     fn = getattr(_lib or lib(), name)
     index = device.index
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the call runs on {device}")
         raw = stream.cuda_stream
     elif _raw_current_stream is not None:
         raw = _raw_current_stream(index)
@@ -465,6 +477,8 @@ def _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, strea
     residual, w_post, gate, then gate_tokens, the addresses of w_pre, h, y, and h, y)."""
     dev, dt = residual.device, residual.dtype
     code = _dt(residual, "residual")
+    if T > _INT_MAX or H > _INT_MAX:
+        _ints(T=T, H=H)
     rows = (T, H)
     pr = _like(residual, "residual", rows, dt, dev)
     pg = py = None
@@ -475,6 +489,7 @@ def _norm_operands(T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, strea
             gate_tokens = max(T, 1) if gate.dim() == 1 else 1
         if gate_tokens < 1:
             raise ValueError(f"gate_tokens must be at least 1, not {gate_tokens}")
+        gate_tokens = min(gate_tokens, max(T, 1))   # beyond T they mean the same
         n = -(-T // gate_tokens)
         pg = _like(gate, "gate", (H,) if gate.dim() == 1 and n <= 1 else (n, H), dt, dev)
     else:
@@ -521,6 +536,7 @@ def fc_dequantize_residual_norm(codes2, s2, z2, T: int, H: int, bits: int, group
                                 stream=None):
     """fc_residual_norm of the dequantized stage-2 payload (as for fc_dequantize_residual,
     but not rounded to 16 bits before the norms) -> (h, y)."""
+    _ints(bits=bits, group2=group2)
     code, pr, pw, pg, gate_tokens, pv, ph, py, h, y = _norm_operands(
         T, H, residual, w_post, gate, gate_tokens, w_pre, h, y, stream)
     dev = residual.device
@@ -542,6 +558,7 @@ def fc_allreduce_emulated_norm(x: torch.Tensor, bits: int, group: int, residual:
     _dev_tensor(x, "x")
     bits2 = bits if bits2 is None else bits2
     R, T, H = x.shape
+    _ints(R=R, bits=bits, bits2=bits2, group=group)
     dev = x.device
     _like(residual, "residual", (T, H), x.dtype, dev)
     code, pr, pw, pg, gate_tokens, pv, ph, py, h, y = _norm_operands(
@@ -562,11 +579,13 @@ def _mx_padded(K: int) -> int:
 def _rows3(t: torch.Tensor, name: str):
     """(R, rows, n) of a 3-D tensor, (1, rows, n) of a 2-D one."""
     s = t.shape
-    if len(s) == 3:
-        return s
-    if len(s) != 2:
+    if len(s) == 2:
+        s = (1, *s)
+    elif len(s) != 3:
         raise ValueError(f"{name} must have 2 or 3 dimensions")
-    return 1, s[0], s[1]
+    if max(s) > _INT_MAX:
+        raise ValueError(f"the dimensions of {name} must fit 32 bits, not {list(s)}")
+    return s
 
 
 def _mx_operand(codes, scales, name: str, device):

@@ -19,6 +19,7 @@
 // them) or, where there are few, as 16-bit values that the workgroup
 // quantizes into LDS while its first weights are on their way (4 ranks, 1 token,
 // K = 2048, H = 8192, bf16: 8.8 us, 4.1 TB/s with the launch's ~2.5 us in it).
+#include "fc_grid.h"
 #include "fc_launch.h"
 #include "fc_mxfp4.h"
 
@@ -40,7 +41,7 @@ struct FewArgs {
     const uint8_t *ac, *as;               // their codes and scales
     const uint8_t *wc, *ws;
     uint16_t *y;
-    int T, K, H;
+    int R, T, K, H;
     int steps;                            // Kp / 128
     int groups;                           // channel groups of a rank
 };
@@ -76,8 +77,9 @@ __global__ __launch_bounds__(kWaves *kWave) void matmul_mxfp4_few_kernel(const F
     const uint32_t row = lane & 15u, kb = lane >> 4;
     const uint32_t code_row = (uint32_t)p.steps * kStepBytes, scale_row = (uint32_t)p.steps * kStepScales;
     constexpr uint32_t kGroup = kWaves / SPLIT * 16;     // channels of a workgroup
-    const uint32_t bid = __builtin_amdgcn_workgroup_id_x();
+    const uint32_t bid = (uint32_t)grid_index();         // R * groups < 2^31
     const uint32_t r = bid / (uint32_t)p.groups;
+    if (r >= (uint32_t)p.R) return;
     const uint32_t h0 = (bid - r * (uint32_t)p.groups) * kGroup + (SPLIT > 1 ? 0u : wave * 16u);
     // this wave's steps
     const uint32_t share = ((uint32_t)p.steps + SPLIT - 1) / SPLIT;
@@ -226,10 +228,10 @@ hipError_t launch(FewArgs p, int R, hipStream_t stream) {
     constexpr int group = kWaves / SPLIT * 16;
     p.groups = (p.H + group - 1) / group;
     const uint64_t blocks = (uint64_t)R * (uint64_t)p.groups;
-    if (blocks * (kWaves * kWave) > 0xFFFFFFFFull) return hipErrorInvalidConfiguration;
+    p.R = R;
     const size_t quant = QUANT ? (size_t)p.T * ((size_t)p.steps * (kStepBytes + kStepScales) + kLdsPad) : 0;
     const size_t parts = SPLIT > 1 ? (size_t)(SPLIT - 1) * NT * kWave * sizeof(f32x4) : 0;
-    hipLaunchKernelGGL((matmul_mxfp4_few_kernel<DT, NT, CH, SPLIT, QUANT>), dim3((unsigned)blocks),
+    hipLaunchKernelGGL((matmul_mxfp4_few_kernel<DT, NT, CH, SPLIT, QUANT>), grid_of_blocks(blocks),
                        dim3(kWaves * kWave), quant > parts ? quant : parts, stream, p);
     return hipGetLastError();
 }

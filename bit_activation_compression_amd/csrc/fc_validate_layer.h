@@ -15,6 +15,7 @@ constexpr int kMxBlock = 32;              // values that share a scale
 constexpr int kMxStep = 128;              // rows are padded to whole matrix-core steps
 constexpr int kMxMaxK = 1 << 22;          // row offsets of a tile fit 32 bits
 constexpr int kMxMaxH = 1 << 24;
+constexpr uint64_t kMxMaxValues = uint64_t(1) << 48;   // of an operand, with its padding: sizes fit 64 bits
 // a rank's operand rows and a grid's tiles are counted in 32 bits
 constexpr long long kMxMaxTiles = 0x7FFFFFFFll;
 
@@ -92,6 +93,7 @@ inline size_t mx_scale_bytes(int R, int rows, int K) {
 
 inline fc_status check_mx(int R, int rows, int K) {
     if (R < 1 || rows < 0 || K < 1 || K > kMxMaxK) return FC_ERR_SHAPE;
+    if ((uint64_t)R * (uint64_t)rows > kMxMaxValues / mx_padded(K)) return FC_ERR_SHAPE;
     return FC_OK;
 }
 

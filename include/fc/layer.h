@@ -88,7 +88,7 @@ fc_status fc_allreduce_emulated_norm(const void *x, fc_dtype dt, int R, int T, i
  *   scales [R][rows][Kp/32]   uint8
  * The values past K are zeros: codes 0 and, where a whole block lies past K,
  * scale 0. A caller that brings codes of its own pads them the same way.
- * Requires R >= 1, rows (T or H) >= 0 and 1 <= K <= 2^22.
+ * Requires R >= 1, rows (T or H) >= 0, 1 <= K <= 2^22 and R * rows * Kp <= 2^48.
  */
 
 /*
@@ -111,9 +111,11 @@ fc_status fc_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int R
  *   y[r][t][h] = round_half_even_to_dt(sum_k a[r][t][k] * w[r][h][k])
  *   a codes and scales [R][T][K], w codes and scales [R][H][K] as above,
  *   y [R][T][H] in dt.
- * Products are exact and summed in binary32 in a fixed order. A NaN scale
- * makes the outputs of its token row (or output channel) NaN.
- * Requires 1 <= H <= 2^24 besides.
+ * Products are exact and summed in binary32, in an order that the call's shape
+ * fixes: calls of different T or R may differ in a sum's last bits. Sums that
+ * overflow binary32 on the way are infinities or NaN. A NaN scale makes the
+ * outputs of its token row (or output channel) NaN.
+ * Requires 1 <= H <= 2^24 and R * ceil(T/16) * ceil(H/16) < 2^31 besides.
  */
 fc_status fc_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,
                           const uint8_t *w_scales, int R, int T, int K, int H, fc_dtype dt,

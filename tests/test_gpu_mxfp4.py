@@ -332,6 +332,24 @@ def test_more_rows_than_a_grid_row():
         del x, codes, scales, out
 
 
+def test_linear_of_more_channels_than_a_grid_row():
+    """A grid row of 2^20 workgroups of 64 channels: 5 x 2^24 channels take more. Sums of
+    128 products of multiples of 1/4 up to 36 are exact in binary32."""
+    R, T, K, H = 5, 2, 128, 1 << 24
+    _say(f"linear {R} x {T} x {K} x {H}")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    wc = torch.randint(0, 256, (R, H, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.full((R, H, K // 32), 127, device="cuda", dtype=torch.uint8)
+    a = torch.randint(-6, 7, (R, T, K), generator=g, device="cuda").to(BF16)
+    y = fc.fc_linear_mxfp4(a, wc, ws)
+    torch.cuda.synchronize()
+    at = torch.tensor([0, 15, 16, 63, 64, (1 << 23) + 5, H - 65, H - 64, H - 1])
+    aq = ref.mx_dequantize(*ref.mx_quantize(a.cpu().double()), K)
+    for r in range(R):
+        w = ref.mx_dequantize(wc[r, at].cpu(), ws[r, at].cpu(), K)
+        assert torch.equal(y[r][:, at].cpu(), (aq[r] @ w.t()).to(BF16)), f"rank {r}"
+
+
 def test_block_chain_captured():
     """The chain below in a graph, with eager work between the replays."""
     R, T, K, H = 4, 24, 512, 1024

@@ -228,6 +228,15 @@ def test_no_tokens():
     assert h.shape == y.shape == (0, 64)
 
 
+@pytest.mark.parametrize("gate_tokens", [5, 1 << 31, (1 << 32) + 1])
+def test_one_gate_row_for_any_longer_span(gate_tokens):
+    d = _cuda(_inputs(5, 200, BF16, 1, 1))
+    d["gate"] = d["gate"][:1]
+    want = fc.fc_residual_norm(**dict(d, gate=d["gate"][0]))
+    got = fc.fc_residual_norm(**dict(d, gate_tokens=gate_tokens))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_binding_refuses():
     d = _cuda(_inputs(4, 64, BF16, 1, 1))
     bad = [

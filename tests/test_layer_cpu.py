@@ -109,6 +109,9 @@ def test_mxfp4_refuses():
     assert Q(a, 0, 1, -1, 128, b, c, None) == 2
     assert Q(a, 0, 1, 8, 0, b, c, None) == 2
     assert Q(a, 0, 1, 8, (1 << 22) + 1, b, c, None) == 2
+    assert Q(a, 0, 1 << 30, 1 << 30, 128, b, c, None) == 2                     # more than 2^48 values
+    assert D(a, b, 1 << 30, 1 << 30, 1 << 22, 0, c, None) == 2
+    assert fc.fc_linear_mxfp4_workspace_bytes(1 << 30, 1 << 30, 1 << 22) == 0
     assert Q(a, 2, 1, 8, 128, b, c, None) == 7
     assert Q(None, 0, 1, 8, 128, b, c, None) == 1
     assert Q(a, 0, 1, 8, 128, b, P(2, 8), None) == 4
@@ -196,6 +199,23 @@ def test_checks_under_sanitizers_match_the_library(tmp_path):
                 assert fc.lib().fc_matmul_mxfp4(P(0), P(1), P(2), P(3), R, T, K, H, 1, P(4), None) == got[1], line
             assert got[2] == -(-K // 128) * 128 and got[3] == got[2] // 2
     assert refused > 1000 and accepted > 100
+
+
+def test_binding_refuses_integers_past_32_bits():
+    """ctypes would cut them down to values the library accepts."""
+    m = torch.empty((4, 64), dtype=torch.bfloat16, device="meta")
+    u8 = torch.empty((4, 32), dtype=torch.uint8, device="meta")
+    u16 = torch.empty((4, 2), dtype=torch.uint16, device="meta")
+    long_ = torch.empty(((1 << 32) + 4, 64), dtype=torch.bfloat16, device="meta")
+    for call in [
+        lambda: fc.fc_dequantize_residual_norm(u8, u16, u16, 4, 64, 4, (1 << 32) + 32, m),
+        lambda: fc.fc_dequantize_residual_norm(u8, u16, u16, 4, 64, 4 - (1 << 32), 32, m),
+        lambda: fc.fc_residual_norm(long_, long_),
+    ]:
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    with pytest.raises(ValueError, match="32 bits"):
+        fc._rows3(long_, "x")
 
 
 # --- the 64-bit statements ---------------------------------------------------
