@@ -269,11 +269,20 @@ void matmul_mxfp4_kernel(const MxArgs p) {
         if (b < NH) f.w[b] = *reinterpret_cast<const u32x4 *>(st + (wh * SH + b * 32) * kStageBytes + o.ch[ks]);
         if (b < NT) f.a[b] = *reinterpret_cast<const u32x4 *>(st + (BH + wt * ST + b * 32) * kStageBytes + o.ch[ks]);
     };
-    // word (0: steps 0 and 1) of stage q (of a scale load's two) in a slot, as read
-    auto words = [&](Words &r, const Offs &o, uint32_t slot, uint32_t q, int word, int b) {
-        const uint8_t *st = lsc + slot * kScales + q * kStageScales + word * 4;
-        if (b < NH) r.w[b] = *reinterpret_cast<const uint32_t *>(st + (wh * SH + b * 32) * kScaleBytes + o.sc);
-        if (b < NT) r.a[b] = *reinterpret_cast<const uint32_t *>(st + (BH + wt * ST + b * 32) * kScaleBytes + o.sc);
+    // both words (of steps 0 and 1, of 2 and 3) of stage q (of a scale load's two)
+    // in a slot, as read
+    auto words = [&](Words &r0, Words &r1, const Offs &o, uint32_t slot, uint32_t q, int b) {
+        const uint8_t *st = lsc + slot * kScales + q * kStageScales;
+        if (b < NH) {
+            const u32x2 v = *reinterpret_cast<const u32x2 *>(st + (wh * SH + b * 32) * kScaleBytes + o.sc);
+            r0.w[b] = v.x;
+            r1.w[b] = v.y;
+        }
+        if (b < NT) {
+            const u32x2 v = *reinterpret_cast<const u32x2 *>(st + (BH + wt * ST + b * 32) * kScaleBytes + o.sc);
+            r0.a[b] = v.x;
+            r1.a[b] = v.y;
+        }
     };
     auto shifted = [&](const Words &r, const Offs &o, bool zero) {
         Words c;
@@ -343,7 +352,7 @@ void matmul_mxfp4_kernel(const MxArgs p) {
 #pragma unroll
                     for (int b = 0; b < NF; ++b) {
                         frag(x.f[ks], o, buf, ks, b);
-                        if (ks < 2) words(x.r[ks], o, slot, q, ks, b);
+                        if (ks == 0) words(x.r[0], x.r[1], o, slot, q, b);
                     }
             };
             auto body = [&](Stage &x, Stage &y, int s) {
@@ -379,7 +388,7 @@ void matmul_mxfp4_kernel(const MxArgs p) {
 #pragma unroll
             for (int b = 0; b < NF; ++b) {
                 frag(f[0], o, cbuf, 0, b);
-                words(r0, o, cslot, 0, 0, b);
+                words(r0, r1, o, cslot, 0, b);
             }
             // step ks with `side`, the reads and loads that overlap it
             auto step = [&](auto odd_, const Words &c, auto &&side) {
@@ -399,17 +408,14 @@ void matmul_mxfp4_kernel(const MxArgs p) {
             for (int s = 0; s < p.stages; ++s) {
                 const uint32_t nbuf = next_buf(), nslot = next_slot(s), nq = stage_of_slot(s + 1);
                 const Words c0 = shifted(r0, o, false);
-                step(kEven, c0, [&](int b) {
-                    frag(f[1], o, cbuf, 1, b);
-                    words(r1, o, cslot, stage_of_slot(s), 1, b);
-                });
+                step(kEven, c0, [&](int b) { frag(f[1], o, cbuf, 1, b); });
                 step(kOdd, c0, [&](int b) { frag(f[0], o, cbuf, 2, b); });
                 const Words c1 = shifted(r1, o, odd_k && s + 1 == p.stages);
                 step(kEven, c1, [&](int b) { frag(f[1], o, cbuf, 3, b); });
                 next_ready();
                 step(kOdd, c1, [&](int b) {
                     frag(f[0], o, nbuf, 0, b);
-                    words(r0, o, nslot, nq, 0, b);
+                    words(r0, r1, o, nslot, nq, b);
                     load_share(b, NH);
                 });
                 load_advance();
