@@ -27,6 +27,13 @@
 //   - rows past H or T lie past the buffer resources and read as zeros. Where K
 //     is an odd multiple of 128, the second half of the last stage is not
 //     fetched (zeros again) and gets scales of 0;
+//   - long calls prefetch into the L2: the workgroups of an XCD that stage the
+//     same rows (4 token tiles x 8 channel tiles run at a time) each touch a
+//     share of the next two stages' lines, in the place of every other scale
+//     load, which has nothing to fetch. Two stages in LDS do not cover the way
+//     past the L2: 70B d_proj slices 980 -> 924 us, 8192 x 8192 x 8192 270 ->
+//     257. Calls of fewer than 4 tiles per compute unit (whose operands the first
+//     tiles bring into the L2) lose: 2 ranks of 4096 x 4096 x 4096 74 -> 77;
 //   - workgroups are persistent: stages of consecutive tiles form one stream,
 //     so the next tile's first stages are in flight during a tile's epilogue.
 //     The tiles are split into one contiguous run per XCD (workgroup b runs on
@@ -62,6 +69,8 @@ constexpr int kScaleStages = 2;           // stages of one scale load
 constexpr int kScaleBytes = kScaleStages * kStageScales;
 constexpr int kSink = 1024;               // where the loads land that only keep the count
 constexpr int kGroupT = 4;                // token tiles per scheduling group
+constexpr int kPrefetchTiles = 4;         // tiles per compute unit from which it is done
+constexpr int kShareA = 8;                // channel tiles among which a token tile's prefetch is shared
 constexpr int kXcds = 8;
 constexpr int kLdsBytes = 160 * 1024;     // LDS of a compute unit
 constexpr uint32_t kPast = 0xFFFFFFF0u;   // an offset past every resource
@@ -105,6 +114,7 @@ struct MxArgs {
     int tiles_t, tiles_h;
     uint32_t total;               // tiles of all ranks
     int grid;
+    bool prefetch;
 };
 
 template <int BH, int BT, int WH, int WT, int NB>
@@ -130,6 +140,7 @@ void matmul_mxfp4_kernel(const MxArgs p) {
     // with one wave per SIMD (LDS for one workgroup, 4 waves) the compiler keeps
     // the accumulators in the other half of the registers
     constexpr bool kAgprs = NW <= 4 && S::kPerCu == 1;
+    constexpr bool kPrefetch = BH * BT >= 256 * 256;   // tiles that many-tile calls use
     static_assert((RW == 32 || RW % 64 == 0) && BH % RW == 0, "a wave stages rows of one operand, whole instructions");
     __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
     uint8_t *const lsc = lds + NB * kCodes;
@@ -139,6 +150,8 @@ void matmul_mxfp4_kernel(const MxArgs p) {
     const uint32_t lane = tid & 63u;
     const int wave = __builtin_amdgcn_readfirstlane((int)(tid >> 6));
     const int wh = wave % WH, wt = wave / WH;
+
+    const bool on_w = wave * RW < BH;              // stages rows of w, or of a
 
     // this XCD's run of tiles, and this workgroup's place in it
     const uint32_t bid = __builtin_amdgcn_workgroup_id_x();
@@ -151,6 +164,7 @@ void matmul_mxfp4_kernel(const MxArgs p) {
 
     struct Tile {
         uint32_t r, h0, t0;
+        uint32_t share;           // this wave's among the workgroups that stage the same rows
     };
     auto tile_at = [&](uint32_t it, Tile &t) -> bool {
         const uint32_t logical = first + it * wgs + bid / kXcds;
@@ -164,11 +178,11 @@ void matmul_mxfp4_kernel(const MxArgs p) {
         const uint32_t gsize = left < kGroupT ? left : kGroupT;
         t.t0 = (grp * kGroupT + in_grp % gsize) * BT;
         t.h0 = in_grp / gsize * BH;
+        t.share = on_w ? in_grp % gsize : in_grp / gsize % kShareA;
         return true;
     };
 
     // --- staging: the load cursor ---
-    const bool on_w = wave * RW < BH;
     struct Source {
         const uint8_t *codes, *scales;     // first row that this wave stages
         uint32_t code_bytes, scale_bytes;  // up to the operand's last row
@@ -191,21 +205,25 @@ void matmul_mxfp4_kernel(const MxArgs p) {
     Tile cur;
     if (!tile_at(0, cur)) return;
     Source src = source_of(cur);
+    uint32_t share = cur.share;
     const bool odd_k = p.code_row % kStageBytes != 0;
 
     // Loads [from, to) of the cursor's stage: a code load covers 8 rows x 8
     // chunks, a scale load 64 rows (or the wave's 32). A stage that shares the
-    // scales of the one before loads nothing, into the sink, instead: the
-    // number of loads in flight stays fixed. The whole offset is a lane's (the
+    // scales of the one before loads into the sink instead (the number of loads
+    // in flight stays fixed): nothing, or a prefetch, 16 bytes of each line of
+    // the wave's share of its rows, two stages of them. The whole offset is a lane's (the
     // resource's bounds check covers it), recomputed for every call (`fresh`)
     // so that none of it is live across the epilogue.
     auto load_part = [&](int from, int to) {
         const __amdgpu_buffer_rsrc_t cres = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<uint8_t *>(src.codes), (short)0, (int)src.code_bytes, kRawBufferFlags);
-        const __amdgpu_buffer_rsrc_t sres = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t *>(src.scales), (short)0, (int)src.scale_bytes, kRawBufferFlags);
-        uint8_t *lc = lds + lbuf * kCodes + (uint32_t)wave * (RW * kStageBytes);
         const bool real = ls % kScaleStages == 0, tail = odd_k && ls + 1 == p.stages;
+        const bool ahead = kPrefetch && p.prefetch && !real;
+        const __amdgpu_buffer_rsrc_t sres = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t *>(ahead ? src.codes : src.scales), (short)0,
+            (int)(ahead ? src.code_bytes : src.scale_bytes), kRawBufferFlags);
+        uint8_t *lc = lds + lbuf * kCodes + (uint32_t)wave * (RW * kStageBytes);
         uint8_t *lw = real ? lsc + lslot * kScales + (uint32_t)wave * (RW * kScaleBytes) : sink;
         const uint32_t l = fresh(lane);
         const uint32_t ch = (l & 7u) ^ (l >> 4);      // the chunk of even loads; odd ones take ch ^ 4
@@ -220,7 +238,13 @@ void matmul_mxfp4_kernel(const MxArgs p) {
                     cres, (__attribute__((address_space(3))) void *)(lc + j * 1024), 16, vo, 0, 0, 0);
             } else {
                 const int i = j - kCodeLoads;
-                const uint32_t vo = real ? (l + 64u * i) * p.scale_row + (uint32_t)ls * kStageScales : kPast;
+                uint32_t vo = real ? (l + 64u * i) * p.scale_row + (uint32_t)ls * kStageScales : kPast;
+                if (ahead && i == 0) {
+                    const uint32_t of = on_w ? kGroupT : kShareA, rows = (uint32_t)RW / of;
+                    const uint32_t st = (uint32_t)ls + 1u + l / rows;
+                    if (l < kScaleStages * rows && st < (uint32_t)p.stages)
+                        vo = (l % rows * of + share) * p.code_row + st * kStageBytes;
+                }
                 if (RW >= 64 || l < RW)
                     __builtin_amdgcn_raw_ptr_buffer_load_lds(
                         sres, (__attribute__((address_space(3))) void *)(lw + (real ? i * 1024 : 0)), 16, vo, 0, 0, 0);
@@ -235,8 +259,12 @@ void matmul_mxfp4_kernel(const MxArgs p) {
         if (ls == p.stages) {
             ls = 0;
             Tile t;
-            if (tile_at(++lt, t)) src = source_of(t);
-            else src.code_bytes = src.scale_bytes = 0;
+            if (tile_at(++lt, t)) {
+                src = source_of(t);
+                share = t.share;
+            } else {
+                src.code_bytes = src.scale_bytes = 0;
+            }
         }
     };
 
@@ -487,6 +515,7 @@ hipError_t launch_tiles(MxArgs p, int R, hipStream_t stream) {
     if (cus <= 0) return hipErrorInvalidDevice;
     if (total > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
     p.total = (uint32_t)total;
+    p.prefetch = total >= (uint64_t)cus * kPrefetchTiles;
     p.grid = (int)(total < (uint64_t)cus * per_cu ? total : (uint64_t)cus * per_cu);
     hipLaunchKernelGGL((matmul_mxfp4_kernel<DT, BH, BT, WH, WT, NB, AHEAD>), dim3((unsigned)p.grid),
                        dim3(WH * WT * 64), 0, stream, p);
