@@ -16,7 +16,8 @@
 //   - the scales are fetched 16 bytes a row at a time, for 2 stages: a load of
 //     8 bytes a row touches as many lines for half the use, and that way the
 //     scales cost the cache more accesses than the codes (70B d_proj slices
-//     1.08 -> 1.03 ms);
+//     1.08 -> 1.03 ms). A stage's scales are read from LDS 8 bytes a row at a time:
+//     at a stride of 16, words would take four bank passes each (1.03 -> 1.02);
 //   - a stage is 4 matrix-core steps of k = 64. Step ks takes blocks 2 ks (lanes
 //     0..31) and 2 ks + 1 (lanes 32..63) of each row: the scale words of a row
 //     (one for steps 0 and 1, one for 2 and 3) are shifted right by a byte in
@@ -40,13 +41,14 @@
 //     XCD b % 8), in groups of 4 token tiles x all channel tiles, so that the
 //     workgroups of an XCD share operands in its L2.
 //
-// What bounds it: the large tile's matrix instructions alone run at 5.3 PFLOP/s
-// with all compute units on random operands (9.8 without the toggling: the
-// power management lowers the clock), and LDS traffic (96 KiB of fragment
-// reads and 32 KiB of fills per k = 128 and workgroup, against 1024 matrix-core
-// cycles) keeps the whole at 3.8 on the 70B d_proj slices (R = 4, T = 8192,
-// K = 7168, H = 8192: 1.02 ms). Four waves of 128 x 128, which read a third
-// less, and stages of half the length, fetched further ahead, were no faster.
+// What bounds it: the 70B d_proj slices (R = 4, T = 8192, K = 7168, H = 8192)
+// take 0.93 ms, 4.1 PFLOP/s. The large tile's matrix instructions alone run at
+// 5.3 PFLOP/s with all compute units on random operands (9.8 without the
+// toggling: the power management lowers the clock). With everything else the
+// clock is 1.6 to 1.8 GHz and the matrix cores are busy 56% of the cycles: a
+// stage is 2048 of theirs, and the waves of a workgroup meet once in each. Four
+// waves of 128 x 128, which read a third less from LDS, and stages of half the
+// length, fetched further ahead, were no faster.
 // Small calls are bound by the latency of the fills: about 128 KiB per compute
 // unit in flight.
 #include <atomic>
@@ -528,7 +530,7 @@ hipError_t launch_tiles(MxArgs p, int R, hipStream_t stream) {
 // with tiles of 64 / 128 / 256 (bf16; R, T, K, H):
 //   1, 2048, 2048, 2048: 15.5 / 12.6 / 19.8     1, 512, 4096, 4096: 14.5 / 16.6 / 29.8
 //   4, 768, 3584, 4096: 55 / 40 / 34            2, 384, 4096, 4096: 19.5 / 17.6 / 30.1
-//   4, 128, 2048, 8192: 16.3 / 14.5 / 20.1      4, 8192, 7168, 8192: 2133 / 1392 / 1025
+//   4, 128, 2048, 8192: 16.3 / 14.5 / 20.1      4, 8192, 7168, 8192: 2133 / 1392 / 930
 // At most one tile per unit leaves the LDS for twice the stages (8 against 4:
 // 1, 256, 4096, 4096 11.6 against 12.1).
 template <int DT>
