@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kBlockThreads) void dequantize_mxfp4_kernel(
     }
 }
 
-// Workgroups (a grid has at most 2^16 rows of them: 2^45 values).
+// Workgroups (a grid has fewer than 2^16 rows of 2^20 of them: 2^48 values).
 bool grid_of(uint64_t units, dim3 *grid) {
     const uint64_t n = (units + kBlockThreads * kUnits - 1) / (kBlockThreads * kUnits);
     *grid = grid_of_blocks(n);

@@ -15,7 +15,7 @@ constexpr int kMxBlock = 32;              // values that share a scale
 constexpr int kMxStep = 128;              // rows are padded to whole matrix-core steps
 constexpr int kMxMaxK = 1 << 22;          // row offsets of a tile fit 32 bits
 constexpr int kMxMaxH = 1 << 24;
-constexpr uint64_t kMxMaxValues = uint64_t(1) << 48;   // of an operand, with its padding: sizes fit 64 bits
+constexpr uint64_t kMxMaxValues = uint64_t(1) << 47;   // of an operand, with its padding: a grid holds them
 // a rank's operand rows and a grid's tiles are counted in 32 bits
 constexpr long long kMxMaxTiles = 0x7FFFFFFFll;
 

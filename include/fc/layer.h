@@ -88,7 +88,7 @@ fc_status fc_allreduce_emulated_norm(const void *x, fc_dtype dt, int R, int T, i
  *   scales [R][rows][Kp/32]   uint8
  * The values past K are zeros: codes 0 and, where a whole block lies past K,
  * scale 0. A caller that brings codes of its own pads them the same way.
- * Requires R >= 1, rows (T or H) >= 0, 1 <= K <= 2^22 and R * rows * Kp <= 2^48.
+ * Requires R >= 1, rows (T or H) >= 0, 1 <= K <= 2^22 and R * rows * Kp <= 2^47.
  */
 
 /*

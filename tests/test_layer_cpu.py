@@ -109,7 +109,7 @@ def test_mxfp4_refuses():
     assert Q(a, 0, 1, -1, 128, b, c, None) == 2
     assert Q(a, 0, 1, 8, 0, b, c, None) == 2
     assert Q(a, 0, 1, 8, (1 << 22) + 1, b, c, None) == 2
-    assert Q(a, 0, 1 << 30, 1 << 30, 128, b, c, None) == 2                     # more than 2^48 values
+    assert Q(a, 0, 1 << 30, 1 << 30, 128, b, c, None) == 2                     # more than 2^47 values
     assert D(a, b, 1 << 30, 1 << 30, 1 << 22, 0, c, None) == 2
     assert fc.fc_linear_mxfp4_workspace_bytes(1 << 30, 1 << 30, 1 << 22) == 0
     assert Q(a, 2, 1, 8, 128, b, c, None) == 7
