@@ -1,9 +1,8 @@
 // Linear layer on MXFP4 operands (include/fc/layer.h): y[r] = a[r] w[r]^T on
 // the scaled matrix cores, v_mfma_scale_f32_32x32x64_f8f6f4 with both operands
 // FP4. Lane l holds row l % 32 of its operand at k = 32 (l / 32) + 0..31: 16
-// bytes of codes and one scale byte, which is one block of the format. The row
-// operand is w (channels), the column operand a (tokens): an accumulator holds
-// channels 8 (v / 4) + 4 (l / 32) + v % 4 of token l % 32.
+// bytes of codes and one scale byte, which is one block of the format. An
+// accumulator holds rows 8 (v / 4) + 4 (l / 32) + v % 4 of column l % 32.
 //
 // Work layout:
 //   - a workgroup owns a BH (channels) x BT (tokens) tile of one rank's
@@ -25,6 +24,15 @@
 //   - small tiles read a stage's fragments from LDS while they multiply the
 //     stage before (their few matrix instructions would not cover the latency
 //     of reads a step ahead); large ones, short of registers, read a step ahead;
+//   - y is written in whole lines: for tiles of 128 and 256 the rows are tokens and
+//     the columns channels, NH i + nb in column i of the NH blocks nb of a wave's
+//     channels (w is staged in that order), so that a lane has NH consecutive
+//     channels of a token and 32 lanes 64 NH bytes of it. With channels as rows,
+//     where a store has 32 bytes of each of 32 tokens, 70B o_proj slices take 338 us
+//     for 297 and 4 x 1024 tokens, K = 3584, H = 4096 39 for 36. Outputs of 128 MiB
+//     and more are stored past the caches (321 -> 297; 2 ranks of 4096 x 4096 x 4096,
+//     64 MiB, 72.3 against 73.5 so). Tiles of 64 have one block: the rows are channels
+//     and two lanes have 32 bytes of a token;
 //   - rows past H or T lie past the buffer resources and read as zeros. Where K
 //     is an odd multiple of 128, the second half of the last stage is not
 //     fetched (zeros again) and gets scales of 0;
@@ -42,7 +50,7 @@
 //     workgroups of an XCD share operands in its L2.
 //
 // What bounds it: the 70B d_proj slices (R = 4, T = 8192, K = 7168, H = 8192)
-// take 0.93 ms, 4.1 PFLOP/s. The large tile's matrix instructions alone run at
+// take 0.92 ms, 4.2 PFLOP/s. The large tile's matrix instructions alone run at
 // 5.3 PFLOP/s with all compute units on random operands (9.8 without the
 // toggling: the power management lowers the clock). With everything else the
 // clock is 1.6 to 1.8 GHz and the matrix cores are busy 56% of the cycles: a
@@ -62,6 +70,9 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+// stores at the alignment of one output
+typedef u32x2 u32x2_u16 __attribute__((aligned(2)));
+typedef uint32_t u32_u16 __attribute__((aligned(2)));
 
 constexpr int kFp4 = 4;                   // operand format of the f8f6f4 instructions
 constexpr int kStageBytes = 128;          // bytes of codes of a row in a stage
@@ -71,6 +82,7 @@ constexpr int kScaleStages = 2;           // stages of one scale load
 constexpr int kScaleBytes = kScaleStages * kStageScales;
 constexpr int kSink = 1024;               // where the loads land that only keep the count
 constexpr int kGroupT = 4;                // token tiles per scheduling group
+constexpr uint64_t kPastCache = uint64_t(128) << 20;   // bytes of y
 constexpr int kPrefetchTiles = 4;         // tiles per compute unit from which it is done
 constexpr int kShareA = 8;                // channel tiles among which a token tile's prefetch is shared
 constexpr int kXcds = 8;
@@ -79,6 +91,7 @@ constexpr uint32_t kPast = 0xFFFFFFF0u;   // an offset past every resource
 // buffer resource word 3 for raw (untyped, unswizzled) 32-bit-addressed
 // buffers on gfx9-family GPUs
 constexpr int kRawBufferFlags = 0x00020000;
+constexpr int kNonTemporal = 2;           // cache policy of a buffer store
 
 // SEL: byte of both scale words (0 or 2)
 template <int SEL>
@@ -116,7 +129,8 @@ struct MxArgs {
     int tiles_t, tiles_h;
     uint32_t total;               // tiles of all ranks
     int grid;
-    bool prefetch;
+    bool prefetch;                // the next stages' lines into the L2
+    bool past_cache;              // y is stored past the caches
 };
 
 template <int BH, int BT, int WH, int WT, int NB>
@@ -143,6 +157,8 @@ void matmul_mxfp4_kernel(const MxArgs p) {
     // the accumulators in the other half of the registers
     constexpr bool kAgprs = NW <= 4 && S::kPerCu == 1;
     constexpr bool kPrefetch = BH * BT >= 256 * 256;   // tiles that many-tile calls use
+    constexpr bool kLines = NH > 1;                // outputs in whole lines
+    static_assert(!kLines || (RW == 64 && (NH == 2 || NH == 4)), "the staging order and the stores below");
     static_assert((RW == 32 || RW % 64 == 0) && BH % RW == 0, "a wave stages rows of one operand, whole instructions");
     __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
     uint8_t *const lsc = lds + NB * kCodes;
@@ -191,9 +207,10 @@ void matmul_mxfp4_kernel(const MxArgs p) {
     };
     auto source_of = [&](const Tile &t) {
         const uint32_t n = on_w ? (uint32_t)p.H : (uint32_t)p.T;           // rows of a rank
-        const uint32_t r0 = on_w ? t.h0 + wave * RW : t.t0 + (wave * RW - BH);
+        const uint32_t span = kLines && on_w ? SH : RW;                    // of rows that it may stage
+        const uint32_t r0 = on_w ? t.h0 + (kLines ? wave * RW / SH * SH : wave * RW) : t.t0 + (wave * RW - BH);
         const uint64_t g = (uint64_t)t.r * n + (r0 < n ? r0 : 0u);
-        const uint32_t rows = r0 < n ? (n - r0 < (uint32_t)RW ? n - r0 : (uint32_t)RW) : 0u;
+        const uint32_t rows = r0 < n ? (n - r0 < span ? n - r0 : span) : 0u;
         Source s;
         s.codes = (on_w ? p.wc : p.ac) + g * p.code_row;
         s.scales = (on_w ? p.ws : p.as) + g * p.scale_row;
@@ -229,23 +246,29 @@ void matmul_mxfp4_kernel(const MxArgs p) {
         uint8_t *lw = real ? lsc + lslot * kScales + (uint32_t)wave * (RW * kScaleBytes) : sink;
         const uint32_t l = fresh(lane);
         const uint32_t ch = (l & 7u) ^ (l >> 4);      // the chunk of even loads; odd ones take ch ^ 4
-        const uint32_t co = (l >> 3) * p.code_row + (uint32_t)ls * kStageBytes;
+        // rows are staged in order, but those of w with kLines: LDS row 32 nb + i of
+        // a span of SH is row NH i + nb of it
+        const bool spread = kLines && on_w;
+        const uint32_t step = spread ? NH : 1u, nb0 = spread ? (uint32_t)wave * RW % SH / 32u : 0u;
+        const uint32_t co = ((l >> 3) * step + nb0) * p.code_row + (uint32_t)ls * kStageBytes;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             if (j < from || j >= to) continue;
             if (j < kCodeLoads) {
                 const uint32_t c = ch ^ (4u * (j & 1));
-                const uint32_t vo = tail && c >= 4u ? kPast : co + 8u * j * p.code_row + (c << 4);
+                const uint32_t row = spread ? 8u * NH * (j % 4) + j / 4 : 8u * j;
+                const uint32_t vo = tail && c >= 4u ? kPast : co + row * p.code_row + (c << 4);
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     cres, (__attribute__((address_space(3))) void *)(lc + j * 1024), 16, vo, 0, 0, 0);
             } else {
                 const int i = j - kCodeLoads;
-                uint32_t vo = real ? (l + 64u * i) * p.scale_row + (uint32_t)ls * kStageScales : kPast;
+                const uint32_t row = spread ? (l & 31u) * NH + nb0 + (l >> 5) : l + 64u * i;
+                uint32_t vo = real ? row * p.scale_row + (uint32_t)ls * kStageScales : kPast;
                 if (ahead && i == 0) {
                     const uint32_t of = on_w ? kGroupT : kShareA, rows = (uint32_t)RW / of;
                     const uint32_t st = (uint32_t)ls + 1u + l / rows;
                     if (l < kScaleStages * rows && st < (uint32_t)p.stages)
-                        vo = (l % rows * of + share) * p.code_row + st * kStageBytes;
+                        vo = (nb0 * 32u + l % rows * of + share) * p.code_row + st * kStageBytes;
                 }
                 if (RW >= 64 || l < RW)
                     __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -350,9 +373,12 @@ void matmul_mxfp4_kernel(const MxArgs p) {
         };
         // row nb of a step's blocks
         auto multiply = [&](auto odd_, int nb, const Frags &f, const Words &c) {
+            constexpr int kSel = decltype(odd_)::value * 2;
 #pragma unroll
-            for (int tb = 0; tb < NT; ++tb)
-                acc[nb][tb] = mfma_mx<decltype(odd_)::value * 2>(f.w[nb], f.a[tb], acc[nb][tb], c.w[nb], c.a[tb]);
+            for (int tb = 0; tb < NT; ++tb) {
+                if constexpr (kLines) acc[nb][tb] = mfma_mx<kSel>(f.a[tb], f.w[nb], acc[nb][tb], c.a[tb], c.w[nb]);
+                else acc[nb][tb] = mfma_mx<kSel>(f.w[nb], f.a[tb], acc[nb][tb], c.w[nb], c.a[tb]);
+            }
         };
         constexpr std::integral_constant<int, 0> kEven;
         constexpr std::integral_constant<int, 1> kOdd;
@@ -454,36 +480,89 @@ void matmul_mxfp4_kernel(const MxArgs p) {
             }
         }
 
-        // epilogue: groups 2 q and 2 q + 1 of 4 channels, swapped between the
-        // halves of the wave, give each lane 8 consecutive channels of a token
-        const uint32_t el = fresh(lane), row = el & 31u, half = el >> 5;
-        uint16_t *const yr = p.y + (uint64_t)cur.r * (uint32_t)p.T * (uint32_t)p.H;
+        if constexpr (kLines) {
+            // A lane has NH consecutive channels of a token, 32 lanes whole lines
+            // of it; accumulator v is token 8 (v / 4) + 4 (lane / 32) + v % 4.
+            uint16_t *const yr = p.y + (uint64_t)cur.r * (uint32_t)p.T * (uint32_t)p.H;
+            const uint32_t el = fresh(lane), t0 = cur.t0 + (uint32_t)(wt * ST), h0 = cur.h0 + (uint32_t)(wh * SH);
+            const uint32_t lt0 = (el >> 5) * 4u, lh0 = (el & 31u) * NH;
+            auto token = [](int tb, int v) { return (uint32_t)(tb * 32 + v / 4 * 8 + v % 4); };
+            auto pair = [&](int tb, int v, int k) { return mx_round2<DT>(acc[2 * k][tb][v], acc[2 * k + 1][tb][v]); };
+            if (p.H % 2 == 0 && h0 + SH <= (uint32_t)p.H) {
+                const uint32_t rows = t0 < (uint32_t)p.T ? ((uint32_t)p.T - t0 < ST ? (uint32_t)p.T - t0 : ST) : 0u;
+                const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc(
+                    yr + (uint64_t)(rows ? t0 : 0u) * (uint32_t)p.H + h0, (short)0,
+                    rows ? (int)((rows * (uint32_t)p.H - h0) * 2u) : 0, kRawBufferFlags);
+                const uint32_t row_bytes = (uint32_t)p.H * 2u;
+                const uint32_t off = lt0 * row_bytes + lh0 * 2u;
+                auto store = [&](auto aux_) {
+                    constexpr int kAux = decltype(aux_)::value;
 #pragma unroll
-        for (int tb = 0; tb < NT; ++tb) {
-            const uint32_t t = cur.t0 + (uint32_t)(wt * ST + tb * 32) + row;
-            uint16_t *yt = yr + (uint64_t)t * (uint32_t)p.H;
+                    for (int tb = 0; tb < NT; ++tb)
 #pragma unroll
-            for (int nb = 0; nb < NH; ++nb) {
+                        for (int v = 0; v < 16; ++v) {
+                            const int o = (int)(off + token(tb, v) * row_bytes);
+                            if constexpr (NH == 4)
+                                __builtin_amdgcn_raw_buffer_store_b64(u32x2{pair(tb, v, 0), pair(tb, v, 1)}, res, o, 0, kAux);
+                            else
+                                __builtin_amdgcn_raw_buffer_store_b32(pair(tb, v, 0), res, o, 0, kAux);
+                        }
+                };
+                if (p.past_cache) store(std::integral_constant<int, kNonTemporal>{});
+                else store(std::integral_constant<int, 0>{});
+            } else {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const f32x16 &v = acc[nb][tb];
-                    uint32_t a0 = mx_round2<DT>(v[8 * q + 0], v[8 * q + 1]), a1 = mx_round2<DT>(v[8 * q + 2], v[8 * q + 3]);
-                    uint32_t b0 = mx_round2<DT>(v[8 * q + 4], v[8 * q + 5]), b1 = mx_round2<DT>(v[8 * q + 6], v[8 * q + 7]);
-                    const auto s0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
-                    const auto s1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
-                    const uint32_t w[4] = {(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
-                    const uint32_t h = cur.h0 + (uint32_t)(wh * SH + nb * 32 + q * 16) + half * 8u;
-                    if (t < (uint32_t)p.T) {
-                        if (h + 8u <= (uint32_t)p.H) {
-                            *reinterpret_cast<u32x4_u16 *>(yt + h) = u32x4{w[0], w[1], w[2], w[3]};
+                for (int tb = 0; tb < NT; ++tb)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) {
+                        const uint32_t t = t0 + lt0 + token(tb, v), h = h0 + lh0;
+                        uint32_t w[NH / 2];
+#pragma unroll
+                        for (int k = 0; k < NH / 2; ++k) w[k] = pair(tb, v, k);
+                        if (t >= (uint32_t)p.T) continue;
+                        uint16_t *yt = yr + (uint64_t)t * (uint32_t)p.H;
+                        if (h + NH <= (uint32_t)p.H) {
+                            if constexpr (NH == 4) *reinterpret_cast<u32x2_u16 *>(yt + h) = u32x2{w[0], w[1]};
+                            else *reinterpret_cast<u32_u16 *>(yt + h) = w[0];
                         } else {
 #pragma unroll
-                            for (uint32_t k = 0; k < 8; ++k)
+                            for (uint32_t k = 0; k < NH; ++k)
                                 if (h + k < (uint32_t)p.H) yt[h + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
                         }
                     }
+            }
+        } else {
+            // groups 2 q and 2 q + 1 of 4 channels, swapped between the
+            // halves of the wave, give each lane 8 consecutive channels of a token
+            const uint32_t el = fresh(lane), row = el & 31u, half = el >> 5;
+            uint16_t *const yr = p.y + (uint64_t)cur.r * (uint32_t)p.T * (uint32_t)p.H;
+#pragma unroll
+            for (int tb = 0; tb < NT; ++tb) {
+                const uint32_t t = cur.t0 + (uint32_t)(wt * ST + tb * 32) + row;
+                uint16_t *yt = yr + (uint64_t)t * (uint32_t)p.H;
+#pragma unroll
+                for (int nb = 0; nb < NH; ++nb) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const f32x16 &v = acc[nb][tb];
+                        uint32_t a0 = mx_round2<DT>(v[8 * q + 0], v[8 * q + 1]), a1 = mx_round2<DT>(v[8 * q + 2], v[8 * q + 3]);
+                        uint32_t b0 = mx_round2<DT>(v[8 * q + 4], v[8 * q + 5]), b1 = mx_round2<DT>(v[8 * q + 6], v[8 * q + 7]);
+                        const auto s0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+                        const auto s1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+                        const uint32_t w[4] = {(uint32_t)s0[0], (uint32_t)s1[0], (uint32_t)s0[1], (uint32_t)s1[1]};
+                        const uint32_t h = cur.h0 + (uint32_t)(wh * SH + nb * 32 + q * 16) + half * 8u;
+                        if (t < (uint32_t)p.T) {
+                            if (h + 8u <= (uint32_t)p.H) {
+                                *reinterpret_cast<u32x4_u16 *>(yt + h) = u32x4{w[0], w[1], w[2], w[3]};
+                            } else {
+#pragma unroll
+                                for (uint32_t k = 0; k < 8; ++k)
+                                    if (h + k < (uint32_t)p.H) yt[h + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+                            }
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
         }
         if (!tile_at(it + 1, cur)) break;
@@ -517,6 +596,7 @@ hipError_t launch_tiles(MxArgs p, int R, hipStream_t stream) {
     if (cus <= 0) return hipErrorInvalidDevice;
     if (total > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
     p.total = (uint32_t)total;
+    p.past_cache = (uint64_t)R * (uint64_t)p.T * (uint64_t)p.H * 2 >= kPastCache;
     p.prefetch = total >= (uint64_t)cus * kPrefetchTiles;
     p.grid = (int)(total < (uint64_t)cus * per_cu ? total : (uint64_t)cus * per_cu);
     hipLaunchKernelGGL((matmul_mxfp4_kernel<DT, BH, BT, WH, WT, NB, AHEAD>), dim3((unsigned)p.grid),
@@ -530,7 +610,7 @@ hipError_t launch_tiles(MxArgs p, int R, hipStream_t stream) {
 // with tiles of 64 / 128 / 256 (bf16; R, T, K, H):
 //   1, 2048, 2048, 2048: 15.5 / 12.6 / 19.8     1, 512, 4096, 4096: 14.5 / 16.6 / 29.8
 //   4, 768, 3584, 4096: 55 / 40 / 34            2, 384, 4096, 4096: 19.5 / 17.6 / 30.1
-//   4, 128, 2048, 8192: 16.3 / 14.5 / 20.1      4, 8192, 7168, 8192: 2133 / 1392 / 930
+//   4, 128, 2048, 8192: 16.3 / 14.5 / 20.1      4, 8192, 7168, 8192: 2133 / 1392 / 920
 // At most one tile per unit leaves the LDS for twice the stages (8 against 4:
 // 1, 256, 4096, 4096 11.6 against 12.1).
 template <int DT>

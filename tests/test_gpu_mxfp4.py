@@ -169,6 +169,22 @@ def test_product_exact(R, T, K, H, dt):
     assert torch.equal(y.cpu(), want.to(torch.float32).to(dt))
 
 
+# four and more of the 256 tiles per compute unit, and outputs past 128 MiB; rows of an odd length, of one
+# that ends inside a tile, and whole ones
+@pytest.mark.parametrize("R,T,K,H,dt", [(8, 2900, 640, 2901, BF16), (8, 2900, 1152, 2900, F16), (2, 8100, 256, 4352, BF16),
+                                        (3, 1000, 384, 1161, F16), (5, 2500, 128, 2570, F16)])
+def test_product_of_many_tiles(R, T, K, H, dt):
+    _say(f"product of many tiles R={R} T={T} K={K} H={H} {dt}")
+    ac, as_, wc, ws = _operands(R, T, K, H, T + K + H, 0)
+    y, check = _guarded((R, T, H), dt)
+    fc.fc_matmul_mxfp4(ac.cuda(), as_.cuda(), wc.cuda(), ws.cuda(), dt, y)
+    torch.cuda.synchronize()
+    check()
+    a, w = ref.mx_dequantize(ac, as_, K).float(), ref.mx_dequantize(wc, ws, K).float()
+    for r in range(R):     # sums that binary32 holds exactly
+        assert torch.equal(y[r].cpu(), (a[r] @ w[r].t().contiguous()).to(dt)), f"rank {r}"
+
+
 @pytest.mark.parametrize("dt", [BF16, F16])
 @pytest.mark.parametrize("R,T,K,H", PRODUCTS)
 def test_product_scales(R, T, K, H, dt):
