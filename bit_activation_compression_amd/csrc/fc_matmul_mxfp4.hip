@@ -53,7 +53,7 @@
 // take 0.92 ms, 4.2 PFLOP/s. The large tile's matrix instructions alone run at
 // 5.3 PFLOP/s with all compute units on random operands (9.8 without the
 // toggling: the power management lowers the clock). With everything else the
-// clock is 1.6 to 1.8 GHz and the matrix cores are busy 56% of the cycles: a
+// clock is 1.6 to 1.7 GHz and the matrix cores are busy 60% of the cycles: a
 // stage is 2048 of theirs, and the waves of a workgroup meet once in each. Four
 // waves of 128 x 128, which read a third less from LDS, and stages of half the
 // length, fetched further ahead, were no faster.
