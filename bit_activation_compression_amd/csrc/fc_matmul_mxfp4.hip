@@ -604,24 +604,30 @@ hipError_t launch_tiles(MxArgs p, int R, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The largest tile whose tiles occupy at least three quarters of the compute
-// units; 64 x 64 where none does, and for at most 64 tokens. Larger tiles move
-// fewer bytes per product, smaller ones spread over more units. Measured, us
-// with tiles of 64 / 128 / 256 (bf16; R, T, K, H):
-//   1, 2048, 2048, 2048: 15.5 / 12.6 / 19.8     1, 512, 4096, 4096: 14.5 / 16.6 / 29.8
-//   4, 768, 3584, 4096: 55 / 40 / 34            2, 384, 4096, 4096: 19.5 / 17.6 / 30.1
-//   4, 128, 2048, 8192: 16.3 / 14.5 / 20.1      4, 8192, 7168, 8192: 2133 / 1392 / 920
-// At most one tile per unit leaves the LDS for twice the stages (8 against 4:
+// Rounds of tiles over the compute units decide: larger tiles move fewer bytes
+// per product, smaller ones waste less of the last round. A round of 256 tiles
+// takes twice one of 128; up to two tiles of 64 per unit take less than a round
+// of 128, and up to five less than two. At most 64 tokens take tiles of 64.
+// Measured, us with tiles of 64 / 128 / 256 (bf16; R, T, K, H):
+//   2, 160, 4096, 5120: 14.2 / 16.9 / 27.3      1, 640, 4096, 4096: 19.4 / 16.9 / 27.9
+//   1, 1408, 4096, 3200: 26.3 / 28.9 / 30.2     3, 256, 4096, 7168: 32.3 / 28.2 / 28.9
+//   2, 1024, 4096, 4096: 42.7 / 30.2 / 30.8     1, 2176, 4096, 4096: 45.2 / 42.6 / 30.5
+//   2, 520, 3584, 6144: 32.9 / 27.3 / 27.7      1, 4352, 4096, 4096: 86.4 / 67.1 / 59.0
+//   4, 128, 2048, 8192: 16.1 / 13.8 / 19.8      4, 8192, 7168, 8192: 2111 / 1378 / 913
+// At most one tile of 64 per unit leaves the LDS for twice the stages (8 against 4:
 // 1, 256, 4096, 4096 11.6 against 12.1).
 template <int DT>
 hipError_t by_shape(const MxArgs &p, int R, hipStream_t stream) {
     const int cus = compute_units();
     if (cus <= 0) return hipErrorInvalidDevice;
+    const uint64_t n = (uint64_t)cus;
     auto tiles = [&](int b) { return (uint64_t)R * (uint64_t)((p.T + b - 1) / b) * (uint64_t)((p.H + b - 1) / b); };
-    const uint64_t full = (uint64_t)cus * 3 / 4;
-    if (p.T > 64 && tiles(256) >= full) return launch_tiles<DT, 256, 256, 2, 4, 2, false>(p, R, stream);
-    if (p.T > 64 && tiles(128) >= full) return launch_tiles<DT, 128, 128, 2, 2, 4, false>(p, R, stream);
-    if (tiles(64) <= (uint64_t)cus) return launch_tiles<DT, 64, 64, 2, 2, 8, true>(p, R, stream);
+    auto rounds = [&](int b) { return (tiles(b) + n - 1) / n; };
+    if (p.T > 64) {
+        if (2 * rounds(256) < rounds(128)) return launch_tiles<DT, 256, 256, 2, 4, 2, false>(p, R, stream);
+        if (tiles(64) > n * (rounds(128) == 2 ? 5 : 2)) return launch_tiles<DT, 128, 128, 2, 2, 4, false>(p, R, stream);
+    }
+    if (tiles(64) <= n) return launch_tiles<DT, 64, 64, 2, 2, 8, true>(p, R, stream);
     return launch_tiles<DT, 64, 64, 2, 2, 4, true>(p, R, stream);
 }
 
