@@ -59,9 +59,9 @@
 // length, fetched further ahead, were no faster.
 // Small calls are bound by the latency of the fills: about 128 KiB per compute
 // unit in flight.
-#include <atomic>
 #include <type_traits>
 
+#include "fc_grid.h"
 #include "fc_launch.h"
 #include "fc_mxfp4.h"
 
@@ -570,22 +570,6 @@ void matmul_mxfp4_kernel(const MxArgs p) {
     wait_loads<0>();   // nothing may land in LDS after the workgroup has ended
 }
 
-// Compute units of the current device, looked up once per device (atomic:
-// host threads may fill the cache at once, with the same value).
-int compute_units() {
-    static std::atomic<int> cached[64] = {};
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return -1;
-    int n = cached[dev].load(std::memory_order_relaxed);
-    if (n <= 0) {
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-            n <= 0)
-            return -1;
-        cached[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
 template <int DT, int BH, int BT, int WH, int WT, int NB, bool AHEAD>
 hipError_t launch_tiles(MxArgs p, int R, hipStream_t stream) {
     constexpr int per_cu = Shape<BH, BT, WH, WT, NB>::kPerCu;
@@ -636,7 +620,7 @@ hipError_t by_shape(const MxArgs &p, int R, hipStream_t stream) {
 hipError_t launch_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                const uint8_t *w_codes, const uint8_t *w_scales, int R, int T, int Kp,
                                int H, int dtype, uint16_t *y, hipStream_t stream) {
-    if (T <= kMxFewTokens && (uint64_t)R * (uint64_t)H < kMxFewChannels)
+    if (mxfp4_few_applies(R, T, Kp, H))
         return launch_matmul_mxfp4_few(a_codes, a_scales, w_codes, w_scales, R, T, Kp, H, dtype, y, stream);
     MxArgs p = {};
     p.ac = a_codes;
