@@ -310,7 +310,9 @@ hipError_t launch_norm_any(NormArgs a, hipStream_t stream) {
     // Two vectors per thread once the device is full of rows: H = 8192 bf16,
     // 512 / 1024 / 2048 rows 9.2 / 12.7 / 24.1 us against 9.0 / 14.2 / 24.6 with
     // one; H = 4096, 512 / 1024 / 8192 rows 5.6 / 9.0 / 43.0 against 5.5 / 8.7 / 44.5.
-    const bool few = (uint64_t)a.T * (uint64_t)a.H < kManyElems;
+    // Rows of at most a wave's 64 vectors would leave half of it idle with two (30000
+    // rows of 256: 23.6 against 13.2).
+    const bool few = nv <= kWave || (uint64_t)a.T * (uint64_t)a.H < kManyElems;
     if (nv <= kNormThreads && few) return launch_norm_rows<DT, SRC, GEN, 1>(a, nv, stream);
     if (nv <= 2 * kNormThreads) return launch_norm_rows<DT, SRC, GEN, 2>(a, nv, stream);
     if (nv <= 4 * kNormThreads) return launch_norm_rows<DT, SRC, GEN, 4>(a, nv, stream);
