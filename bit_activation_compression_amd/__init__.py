@@ -653,6 +653,7 @@ def fc_matmul_mxfp4(a_codes, a_scales, w_codes, w_scales, dtype: torch.dtype, y=
 
 
 def fc_linear_mxfp4_workspace_bytes(R: int, T: int, K: int) -> int:
+    _ints(R=R, T=T, K=K)
     return (_lib or lib()).fc_linear_mxfp4_workspace_bytes(R, T, K)
 
 
@@ -673,7 +674,7 @@ def fc_linear_mxfp4(a: torch.Tensor, w_codes, w_scales, y=None, workspace=None, 
         py = _like(y, "y", shape, a.dtype, dev)
     have, pk = 0, None
     if workspace is None:
-        need = fc_linear_mxfp4_workspace_bytes(R, T, K)
+        need = (_lib or lib()).fc_linear_mxfp4_workspace_bytes(R, T, K)   # integers checked by _rows3
         if need:
             workspace = _empty(a, need, torch.uint8, stream)
             have, pk = need, workspace.data_ptr()

@@ -218,6 +218,16 @@ def test_binding_refuses_integers_past_32_bits():
         fc._rows3(long_, "x")
 
 
+def test_workspace_query_refuses_integers_past_32_bits():
+    """(1, 2^32 + 8, 8192), cut to 32 bits, would be the workspace of 8 tokens."""
+    for args in [(1, (1 << 32) + 8, 8192), ((1 << 32) + 1, 300, 128), (1, 300, (1 << 32) + 128), (1, 8 - (1 << 32), 8192)]:
+        with pytest.raises(ValueError, match="32 bits"):
+            fc.fc_linear_mxfp4_workspace_bytes(*args)
+    # the largest that fit: refused by the library, and within its limits
+    assert fc.fc_linear_mxfp4_workspace_bytes(2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1) == 0
+    assert fc.fc_linear_mxfp4_workspace_bytes(1, 2 ** 31 - 1, 128) >= (2 ** 31 - 1) * 68
+
+
 # --- the 64-bit statements ---------------------------------------------------
 
 def test_reference_quantizer_on_the_grid_ties_and_limits():
