@@ -97,11 +97,12 @@ inline fc_status check_mx(int R, int rows, int K) {
     return FC_OK;
 }
 
-// Tiles of the product's grids: 16 x 16 outputs is the smallest tile of any.
+// Both operands, and the tiles of the product's grids: 16 x 16 outputs is the
+// smallest tile of any.
 inline fc_status check_mx_product(int R, int T, int K, int H) {
     fc_status st = check_mx(R, T, K);
     if (st != FC_OK) return st;
-    if (H < 1 || H > kMxMaxH) return FC_ERR_SHAPE;
+    if (H < 1 || H > kMxMaxH || check_mx(R, H, K) != FC_OK) return FC_ERR_SHAPE;
     const long long tt = ((long long)T + 15) / 16, th = ((long long)H + 15) / 16;
     if (tt * th > kMxMaxTiles / R) return FC_ERR_SHAPE;
     return FC_OK;

@@ -228,6 +228,19 @@ def test_workspace_query_refuses_integers_past_32_bits():
     assert fc.fc_linear_mxfp4_workspace_bytes(1, 2 ** 31 - 1, 128) >= (2 ** 31 - 1) * 68
 
 
+def test_weights_of_more_than_2_to_47_values_are_refused():
+    """The limit on an operand's values holds for w as for a; R = 2 of the largest H and K meets it."""
+    L, (a, b, c, d, e, f) = fc.lib(), (P(i) for i in range(6))
+    H, K = 1 << 24, 1 << 22
+    for T in (0, 1):
+        assert L.fc_matmul_mxfp4(a, b, c, d, 3, T, K, H, 0, e, None) == 2
+        assert L.fc_linear_mxfp4(a, b, c, 0, 3, T, K, H, d, e, 1 << 30, None) == 2
+        assert L.fc_matmul_mxfp4(a, b, c, d, 1024, T, K, H // 512 + 1, 0, e, None) == 2
+    assert L.fc_matmul_mxfp4(a, b, c, d, 2, 0, K, H, 0, e, None) == 0
+    assert L.fc_linear_mxfp4(a, b, c, 0, 2, 0, K, H, d, e, 0, None) == 0
+    assert L.fc_matmul_mxfp4(a, b, c, d, 1024, 0, K, H // 512, 0, e, None) == 0
+
+
 # --- the 64-bit statements ---------------------------------------------------
 
 def test_reference_quantizer_on_the_grid_ties_and_limits():
