@@ -9,6 +9,7 @@
 #include "fc.h"
 #include "fc/layer.h"
 #include "fc_launch.h"
+#include "fc_mxfp4_dispatch.h"
 #include "fc_validate.h"
 #include "fc_validate_layer.h"
 

@@ -101,18 +101,12 @@ hipError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, 
 hipError_t launch_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                const uint8_t *w_codes, const uint8_t *w_scales, int R, int T, int Kp,
                                int H, int dtype, uint16_t *y, hipStream_t stream);
-// The same for few tokens of few channels, which would not fill the device with
-// tiles (launch_matmul_mxfp4 chooses): up to 64 tokens in one round of 16 channels
-// of all ranks per compute unit, up to 24 in two of long rows. us against tiles,
-// bf16; R, T, K, H: 1, 16, 4096, 4096 6.4 / 10.1; 1, 64, 4096, 4096 10.0 / 10.4; 1, 64,
-// 4096, 6144 17.0 / 11.2; 1, 17, 8192, 8192 14.5 / 16.3; 1, 32, 8192, 8192 18.0 / 16.5.
-bool mxfp4_few_applies(int R, int T, int Kp, int H);
+// The same for few tokens (launch_matmul_mxfp4 chooses, fc_mxfp4_dispatch.h).
 hipError_t launch_matmul_mxfp4_few(const uint8_t *a_codes, const uint8_t *a_scales,
                                    const uint8_t *w_codes, const uint8_t *w_scales, int R, int T, int Kp,
                                    int H, int dtype, uint16_t *y, hipStream_t stream);
 // The product of 16-bit activations a [R][T][K], quantized in the kernel, for
-// calls with few of them (mxfp4_quantizes_in_place).
-bool mxfp4_quantizes_in_place(int T, int Kp);
+// calls with few of them (mxfp4_quantizes_in_place, fc_mxfp4_dispatch.h).
 hipError_t launch_linear_mxfp4_few(const uint16_t *a, const uint8_t *w_codes, const uint8_t *w_scales,
                                    int R, int T, int K, int Kp, int H, int dtype, uint16_t *y,
                                    hipStream_t stream);

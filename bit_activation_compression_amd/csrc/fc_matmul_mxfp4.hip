@@ -64,6 +64,7 @@
 #include "fc_grid.h"
 #include "fc_launch.h"
 #include "fc_mxfp4.h"
+#include "fc_mxfp4_dispatch.h"
 
 namespace fc {
 namespace {
@@ -571,13 +572,11 @@ void matmul_mxfp4_kernel(const MxArgs p) {
 }
 
 template <int DT, int BH, int BT, int WH, int WT, int NB, bool AHEAD>
-hipError_t launch_tiles(MxArgs p, int R, hipStream_t stream) {
+hipError_t launch_tiles(MxArgs p, int R, int cus, hipStream_t stream) {
     constexpr int per_cu = Shape<BH, BT, WH, WT, NB>::kPerCu;
-    p.tiles_t = (p.T + BT - 1) / BT;
-    p.tiles_h = (p.H + BH - 1) / BH;
+    p.tiles_t = mxfp4_tiles(p.T, BT);
+    p.tiles_h = mxfp4_tiles(p.H, BH);
     const uint64_t total = (uint64_t)R * (uint64_t)p.tiles_t * (uint64_t)p.tiles_h;
-    const int cus = compute_units();
-    if (cus <= 0) return hipErrorInvalidDevice;
     if (total > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
     p.total = (uint32_t)total;
     p.past_cache = (uint64_t)R * (uint64_t)p.T * (uint64_t)p.H * 2 >= kPastCache;
@@ -588,31 +587,15 @@ hipError_t launch_tiles(MxArgs p, int R, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Rounds of tiles over the compute units decide: larger tiles move fewer bytes
-// per product, smaller ones waste less of the last round. A round of 256 tiles
-// takes twice one of 128; up to two tiles of 64 per unit take less than a round
-// of 128, and up to five less than two. At most 64 tokens take tiles of 64.
-// Measured, us with tiles of 64 / 128 / 256 (bf16; R, T, K, H):
-//   2, 160, 4096, 5120: 14.2 / 16.9 / 27.3      1, 640, 4096, 4096: 19.4 / 16.9 / 27.9
-//   1, 1408, 4096, 3200: 26.3 / 28.9 / 30.2     3, 256, 4096, 7168: 32.3 / 28.2 / 28.9
-//   2, 1024, 4096, 4096: 42.7 / 30.2 / 30.8     1, 2176, 4096, 4096: 45.2 / 42.6 / 30.5
-//   2, 520, 3584, 6144: 32.9 / 27.3 / 27.7      1, 4352, 4096, 4096: 86.4 / 67.1 / 59.0
-//   4, 128, 2048, 8192: 16.1 / 13.8 / 19.8      4, 8192, 7168, 8192: 2111 / 1378 / 913
-// At most one tile of 64 per unit leaves the LDS for twice the stages (8 against 4:
-// 1, 256, 4096, 4096 11.6 against 12.1).
 template <int DT>
-hipError_t by_shape(const MxArgs &p, int R, hipStream_t stream) {
-    const int cus = compute_units();
-    if (cus <= 0) return hipErrorInvalidDevice;
-    const uint64_t n = (uint64_t)cus;
-    auto tiles = [&](int b) { return (uint64_t)R * (uint64_t)((p.T + b - 1) / b) * (uint64_t)((p.H + b - 1) / b); };
-    auto rounds = [&](int b) { return (tiles(b) + n - 1) / n; };
-    if (p.T > 64) {
-        if (2 * rounds(256) < rounds(128)) return launch_tiles<DT, 256, 256, 2, 4, 2, false>(p, R, stream);
-        if (tiles(64) > n * (rounds(128) == 2 ? 5 : 2)) return launch_tiles<DT, 128, 128, 2, 2, 4, false>(p, R, stream);
+hipError_t by_shape(const MxArgs &p, int R, int cus, hipStream_t stream) {
+    switch (mxfp4_tile(R, p.T, p.H, cus)) {
+    case Mxfp4Tile::k256: return launch_tiles<DT, 256, 256, 2, 4, 2, false>(p, R, cus, stream);
+    case Mxfp4Tile::k128: return launch_tiles<DT, 128, 128, 2, 2, 4, false>(p, R, cus, stream);
+    case Mxfp4Tile::k64: return launch_tiles<DT, 64, 64, 2, 2, 4, true>(p, R, cus, stream);
+    case Mxfp4Tile::k64Deep: return launch_tiles<DT, 64, 64, 2, 2, 8, true>(p, R, cus, stream);
     }
-    if (tiles(64) <= n) return launch_tiles<DT, 64, 64, 2, 2, 8, true>(p, R, stream);
-    return launch_tiles<DT, 64, 64, 2, 2, 4, true>(p, R, stream);
+    return hipErrorInvalidConfiguration;
 }
 
 }  // namespace
@@ -620,7 +603,9 @@ hipError_t by_shape(const MxArgs &p, int R, hipStream_t stream) {
 hipError_t launch_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                const uint8_t *w_codes, const uint8_t *w_scales, int R, int T, int Kp,
                                int H, int dtype, uint16_t *y, hipStream_t stream) {
-    if (mxfp4_few_applies(R, T, Kp, H))
+    const int cus = compute_units();
+    if (cus <= 0) return hipErrorInvalidDevice;
+    if (mxfp4_few_tokens(R, T, Kp / kMxStepElems, H, cus))
         return launch_matmul_mxfp4_few(a_codes, a_scales, w_codes, w_scales, R, T, Kp, H, dtype, y, stream);
     MxArgs p = {};
     p.ac = a_codes;
@@ -633,7 +618,7 @@ hipError_t launch_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
     p.stages = (Kp / kMxStepElems + 1) / 2;
     p.code_row = (uint32_t)Kp / 2;
     p.scale_row = (uint32_t)Kp / kMxBlockElems;
-    return dtype == 0 ? by_shape<0>(p, R, stream) : by_shape<1>(p, R, stream);
+    return dtype == 0 ? by_shape<0>(p, R, cus, stream) : by_shape<1>(p, R, cus, stream);
 }
 
 }  // namespace fc

@@ -10,7 +10,7 @@
 // such chunk ahead, so that a wave has up to 2 CH KiB of weights in flight.
 // The scales of 4 steps of a row are one 16-byte load.
 //
-// Where the channels alone would leave the device empty (split_rounds), the
+// Where the channels alone would leave the device empty (mxfp4_split_rounds), the
 // SPLIT waves of a workgroup share 16 channels and take SPLIT runs of steps;
 // the first adds the others' partial sums from LDS, in their order. (1 rank, 1
 // token, K = 4096, H = 4096, bf16: 4.5 us, 9.1 unsplit; split over 8 waves 5.6.)
@@ -22,6 +22,7 @@
 #include "fc_grid.h"
 #include "fc_launch.h"
 #include "fc_mxfp4.h"
+#include "fc_mxfp4_dispatch.h"
 
 namespace fc {
 namespace {
@@ -61,18 +62,13 @@ __device__ __forceinline__ u32x4 buffer16(const __amdgpu_buffer_rsrc_t &r, uint3
 // the partial sums of split waves; sized at launch
 extern __shared__ __attribute__((aligned(16))) uint8_t few_lds[];
 
-// Most activations of a rank that the kernel quantizes itself, which saves the
-// quantizer's launch: 4 ranks, K = 2048, H = 8192, bf16, 4 / 6 / 8 tokens 9.5 /
-// 10.5 / 11.0 us against 12.1 / 12.3 / 12.3 with it; twice as many are no faster.
-constexpr int kQuantizeMost = 16384;
 constexpr int kWaves = 4;
-constexpr int kLongSteps = 32;            // of k = 128, see split_rounds
 
-// QUANT: quantize the 16-bit activations (T * Kp <= kQuantizeMost)
+// QUANT: quantize the 16-bit activations (T * Kp <= kMxfp4QuantizeMost)
 template <int DT, int NT, int CH, int SPLIT, bool QUANT>
 __global__ __launch_bounds__(kWaves *kWave) void matmul_mxfp4_few_kernel(const FewArgs p) {
     static_assert(CH % 4 == 0 && (!QUANT || NT == 1), "");
-    constexpr int kUnits = kQuantizeMost / (kWaves * kWave * kLaneElems);   // that a thread quantizes
+    constexpr int kUnits = kMxfp4QuantizeMost / (kWaves * kWave * kLaneElems);   // that a thread quantizes
     const uint32_t tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63u;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
     const uint32_t row = lane & 15u, kb = lane >> 4;
@@ -237,17 +233,6 @@ hipError_t launch(FewArgs p, int R, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Rounds of workgroups over the compute units with split waves, where those are
-// worth it: one, or two of long rows. us split / unsplit / tiles (fc_matmul_mxfp4,
-// 1 token, 1 rank, bf16; K, H): 4096, 4096 5.4 / 9.3 / 10.1; 4096, 8192 9.3 / 9.5 /
-// 10.5; 8192, 8192 11.0 / 15.2 / 16.3; 1024, 8192 7.1 / 5.2 / 5.9; 4096, 14336 15.8 /
-// 9.9 / 11.1. 0: not worth it (or no device).
-int split_rounds(int R, int H, int steps) {
-    const int64_t groups = (int64_t)R * ((H + 15) / 16), cus = compute_units();
-    if (groups <= cus) return 1;
-    return groups <= 2 * cus && steps >= kLongSteps ? 2 : 0;
-}
-
 template <int DT>
 hipError_t by_tokens(const FewArgs &p, int R, hipStream_t stream) {
     if (p.T <= 16) return launch<DT, 1, 8, kWaves, false>(p, R, stream);
@@ -257,20 +242,13 @@ hipError_t by_tokens(const FewArgs &p, int R, hipStream_t stream) {
 
 template <int DT>
 hipError_t quantizing(const FewArgs &p, int R, hipStream_t stream) {
-    if (split_rounds(R, p.H, p.steps) != 0) return launch<DT, 1, 8, kWaves, true>(p, R, stream);
+    const int cus = compute_units();
+    if (cus <= 0) return hipErrorInvalidDevice;
+    if (mxfp4_split_rounds(R, p.H, p.steps, cus) != 0) return launch<DT, 1, 8, kWaves, true>(p, R, stream);
     return launch<DT, 1, 8, 1, true>(p, R, stream);
 }
 
 }  // namespace
-
-bool mxfp4_few_applies(int R, int T, int Kp, int H) {
-    const int rounds = split_rounds(R, H, Kp / kMxStepElems);
-    return rounds == 1 ? T <= 64 : rounds == 2 && T <= 24;
-}
-
-bool mxfp4_quantizes_in_place(int T, int Kp) {
-    return T <= 16 && (int64_t)T * Kp <= kQuantizeMost;
-}
 
 hipError_t launch_linear_mxfp4_few(const uint16_t *a, const uint8_t *w_codes, const uint8_t *w_scales,
                                    int R, int T, int K, int Kp, int H, int dtype, uint16_t *y,

@@ -438,3 +438,27 @@ def test_block_chain():
     q = ref.mx_quantize(n.cpu().double())
     want, mag = ref.mx_product(ref.mx_dequantize(*q, H)[None], ref.mx_dequantize(vc.cpu(), vs.cpu(), H)[None])
     ref.assert_within(out, want[0], BF16, mag[0] * (H * 2.0 ** -23), "next projection")
+
+
+def test_product_of_the_most_tokens():
+    """2^31 - 1 tokens, whose tiles' counts pass 32 bits where they are rounded up: 128 GiB of codes.
+    Rows of ones at sampled tokens, zeros elsewhere; w = 1 gives K for the former."""
+    T, K, dev = (1 << 31) - 1, 128, "cuda"
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 170 << 30:
+        pytest.skip("needs 170 GiB of free device memory")
+    _say(f"product of {T} tokens")
+    at = torch.tensor([0, 1, 127, 128, (1 << 30) + 5, T - 257, T - 256, T - 129, T - 128, T - 1], device=dev)
+    ac = torch.zeros((T, K // 2), dtype=torch.uint8, device=dev)
+    as_ = torch.full((T, K // 32), 127, dtype=torch.uint8, device=dev)
+    ac[at] = 0x22
+    wc = torch.full((1, K // 2), 0x22, dtype=torch.uint8, device=dev)
+    ws = torch.full((1, K // 32), 127, dtype=torch.uint8, device=dev)
+    y, check = _guarded((T, 1), BF16)
+    fc.fc_matmul_mxfp4(ac, as_, wc, ws, BF16, y)
+    torch.cuda.synchronize()
+    check()
+    assert (y[at] == K).all()
+    assert int(torch.count_nonzero(y)) == len(at)
+    del ac, as_, wc, ws, y, check
+    torch.cuda.empty_cache()
