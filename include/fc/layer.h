@@ -111,10 +111,11 @@ fc_status fc_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int R
  *   y[r][t][h] = round_half_even_to_dt(sum_k a[r][t][k] * w[r][h][k])
  *   a codes and scales [R][T][K], w codes and scales [R][H][K] as above,
  *   y [R][T][H] in dt.
- * Products are exact and summed in binary32, in an order that the call's shape
- * fixes: calls of different T or R may differ in a sum's last bits. Sums that
- * overflow binary32 on the way are infinities or NaN. A NaN scale makes the
- * outputs of its token row (or output channel) NaN.
+ * Products are summed in binary32, in an order that the call's shape fixes:
+ * calls of different T or R may differ in a sum's last bits. Subnormal sums are
+ * kept, what lies below 2^-149 is rounded away (both scales near 2^-127: the
+ * outputs are zeros), and sums that overflow on the way are infinities or NaN.
+ * A NaN scale makes the outputs of its token row (or output channel) NaN.
  * Requires 1 <= H <= 2^24 and R * ceil(T/16) * ceil(H/16) < 2^31 besides.
  */
 fc_status fc_matmul_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,

@@ -462,3 +462,26 @@ def test_product_of_the_most_tokens():
     assert int(torch.count_nonzero(y)) == len(at)
     del ac, as_, wc, ws, y, check
     torch.cuda.empty_cache()
+
+
+# one shape for each kernel of the product on 256 compute units, but for the many-tile ones
+TARGETS = {"few": (1, 64), "few of 64 tokens": (64, 64), "64, 8 stages": (300, 512), "64, 4 stages": (1408, 3200),
+           "128": (1024, 4096), "256": (2176, 4096)}
+
+
+@pytest.mark.parametrize("target", TARGETS)
+def test_small_scales(target):
+    """Exponents that sum to e: sums are multiples of 2^(e - 2), which binary32 holds, among them
+    subnormal ones, and one rounding takes them to bf16's subnormals. With both scales 2^-127 every
+    sum is far below 2^-149: zeros."""
+    (T, H), K = TARGETS[target], 256
+    ac, as_, wc, ws = _operands(1, T, K, H, 5, 0)
+    as_[...] = 0
+    for e in (-125, -135, -140, -254):
+        _say(f"small scales {target}: 2^{e}")
+        ws[...] = e + 254
+        y = fc.fc_matmul_mxfp4(ac.cuda(), as_.cuda(), wc.cuda(), ws.cuda(), BF16).cpu()
+        want, _ = ref.mx_product(ref.mx_dequantize(ac, as_, K), ref.mx_dequantize(wc, ws, K))
+        want = want.to(torch.float32).to(BF16)
+        assert torch.equal(y, want)
+        assert bool((want != 0).any()) == (e != -254)
