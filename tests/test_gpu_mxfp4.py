@@ -485,3 +485,115 @@ def test_small_scales(target):
         want = want.to(torch.float32).to(BF16)
         assert torch.equal(y, want)
         assert bool((want != 0).any()) == (e != -254)
+
+
+@pytest.mark.parametrize("target", TARGETS)
+@pytest.mark.parametrize("a_byte,w_byte", [(0, 247), (247, 0), (254, 0), (0, 254), (254, 1)])
+def test_extreme_scales_in_every_kernel(target, a_byte, w_byte):
+    """Neither scale alone leaves a product in binary32's range."""
+    (T, H), K = TARGETS[target], 256
+    _say(f"extreme scales {target} {a_byte} {w_byte}")
+    ac, as_, wc, ws = _operands(1, T, K, H, 6, 0)
+    as_[...] = a_byte
+    ws[...] = w_byte
+    y = fc.fc_matmul_mxfp4(ac.cuda(), as_.cuda(), wc.cuda(), ws.cuda(), BF16)
+    want, _ = ref.mx_product(ref.mx_dequantize(ac, as_, K), ref.mx_dequantize(wc, ws, K))
+    assert torch.equal(y.cpu(), want.to(torch.float32).to(BF16))
+
+
+# (R, T, H) for each kernel; the last walks many tiles of 256 with the L2 prefetch
+NAN_SHAPES = [(1, 1, 64), (1, 50, 64), (1, 64, 130), (1, 300, 512), (1, 1408, 3200), (3, 30, 8260), (1, 1024, 4096),
+              (1, 2176, 4096), (2, 1000, 4360), (8, 2900, 2900)]
+
+
+@pytest.mark.parametrize("K", [128, 384, 512, 640, 1152])
+@pytest.mark.parametrize("R,T,H", NAN_SHAPES)
+def test_nan_scales_in_every_kernel(R, T, H, K):
+    """NaN scales in the first and the last block of rows at the tiles' borders make those rows (of a)
+    and channels (of w) NaN and no other: the row before one whose first scale is NaN ends in the
+    same 16 bytes of scales where K is an odd multiple of 128. Elsewhere y is as without them."""
+    _say(f"NaN scales R={R} T={T} K={K} H={H}")
+    g = torch.Generator(device="cuda").manual_seed(T + K)
+    def side(rows):
+        codes = torch.randint(0, 256, (R, rows, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+        scales = torch.randint(126, 129, (R, rows, K // 32), generator=g, device="cuda", dtype=torch.int32).to(torch.uint8)
+        return codes, scales
+    ac, as_ = side(T)
+    wc, ws = side(H)
+    clean = fc.fc_matmul_mxfp4(ac, as_, wc, ws, BF16)
+    bad = torch.zeros((R, T, H), dtype=torch.bool, device="cuda")
+    def plant(scales, n, at):
+        rows = sorted({r for r in at if r < n} | {n - 1}) if n > 1 else []
+        for i, r in enumerate(rows):
+            scales[i % R, r, 0 if i % 2 == 0 else -1] = 255
+        return [(i % R, r) for i, r in enumerate(rows)]
+    at = [1, 17, 32, 63, 64, 127, 128, 191, 255, 256, 511, 512, 640]
+    for r, t in plant(as_, T, at):
+        bad[r, t] = True
+    for r, h in plant(ws, H, [c + 1 for c in at] + [2048, 2304]):
+        bad[r, :, h] = True
+    y, check = _guarded((R, T, H), BF16)
+    fc.fc_matmul_mxfp4(ac, as_, wc, ws, BF16, y)
+    torch.cuda.synchronize()
+    check()
+    assert torch.isfinite(clean).all()
+    assert torch.equal(torch.isnan(y), bad)
+    assert torch.equal(torch.where(bad, 0.0, y.float()), torch.where(bad, 0.0, clean.float()))
+
+
+@pytest.mark.parametrize("T,K,H", [(1, 384, 64), (5, 384, 4200), (1, 4224, 4200), (12, 1152, 17000)])
+def test_nan_activations_quantized_in_place(T, K, H):
+    """fc_linear_mxfp4 where the product quantizes: a NaN activation and NaN scales of w."""
+    _say(f"linear NaN T={T} K={K} H={H}")
+    g = torch.Generator().manual_seed(T)
+    a = torch.randn((1, T, K), generator=g).to(BF16)
+    a[0, T // 2, K - 1] = float("nan")
+    _, _, wc, ws = _operands(1, 1, K, H, 1, 1)
+    bad = torch.zeros(1, T, H, dtype=torch.bool)
+    bad[:, T // 2] = True
+    for h, block in ((1, 0), (16, -1), (H - 1, 0)):
+        ws[0, h, block] = 255
+        bad[..., h] = True
+    assert fc.fc_linear_mxfp4_workspace_bytes(1, T, K) == 0
+    y, check = _guarded((1, T, H), BF16)
+    fc.fc_linear_mxfp4(a.cuda(), wc.cuda(), ws.cuda(), y)
+    torch.cuda.synchronize()
+    check()
+    assert torch.equal(torch.isnan(y.cpu()), bad)
+
+
+# Tiles of 64 two to a compute unit, more of them than fit the device at once, whole and odd multiples of
+# 128, one and several stages; the same of the tiles of 128 and 256; split waves in two rounds, with each number of token blocks
+SMALL_TILES = [(1, 1408, 128, 3200), (1, 1408, 384, 3200), (1, 1350, 1000, 3230), (1, 1390, 1280, 3137), (4, 40, 384, 8300),
+               (4, 64, 896, 8257), (9, 3, 256, 4100), (9, 50, 640, 4101), (3, 17, 1408, 12000)]
+LARGE_TILES = [(2, 2300, 512, 1700), (2, 2300, 1280, 1702), (8, 1300, 512, 2100), (8, 1300, 384, 2101)]
+TWO_ROUNDS = [(1, 1, 4096, 4200), (1, 3, 4100, 8192), (2, 16, 4224, 2100), (1, 17, 4096, 4097), (1, 24, 4352, 8191), (2, 20, 4100, 4096)]
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("R,T,K,H", SMALL_TILES + LARGE_TILES + TWO_ROUNDS)
+def test_product_and_linear_in_every_kernel(R, T, K, H, dt):
+    """Both calls where the sums are exact (K * 36 * 4 and, with activations that quantize to
+    magnitudes of up to 12, K * 72 * 4 below 2^24 quarters)."""
+    _say(f"every kernel R={R} T={T} K={K} H={H} {dt}")
+    assert K * 72 * 4 < 2 ** 24
+    ac, as_, wc, ws = _operands(R, T, K, H, T + K + H, 0)
+    w = ref.mx_dequantize(wc, ws, K).float()
+    wc, ws = wc.cuda(), ws.cuda()
+    y, check = _guarded((R, T, H), dt)
+    fc.fc_matmul_mxfp4(ac.cuda(), as_.cuda(), wc, ws, dt, y)
+    torch.cuda.synchronize()
+    check()
+    a = ref.mx_dequantize(ac, as_, K).float()
+    for r in range(R):     # sums that binary32 holds exactly
+        assert torch.equal(y[r].cpu(), (a[r] @ w[r].t().contiguous()).to(dt)), f"rank {r}"
+    g = torch.Generator().manual_seed(T)
+    x = torch.randint(-12, 13, (R, T, K), generator=g).to(dt)
+    x[..., ::32] = 4
+    y, check = _guarded((R, T, H), dt)
+    fc.fc_linear_mxfp4(x.cuda(), wc, ws, y)
+    torch.cuda.synchronize()
+    check()
+    a = ref.mx_dequantize(*ref.mx_quantize(x.double()), K).float()
+    for r in range(R):
+        assert torch.equal(y[r].cpu(), (a[r] @ w[r].t().contiguous()).to(dt)), f"rank {r}"

@@ -50,3 +50,27 @@ def test_channels_up_to_the_largest_count(choose, H):
     (product, linear, *_), (wide, *_) = choose([(1, 1, 128, H), (127, 16, 128, H)])
     assert (product, linear) == (("split1", "quantize1") if H <= 256 * 16 else ("64", "quantize0"))
     assert wide == ("split1" if 127 * -(-H // 16) <= 256 else "64")
+
+
+def test_gpu_tests_reach_every_kernel(choose):
+    """The shapes of test_gpu_mxfp4.py through the rules: every kernel, the tiles with one stage, with odd
+    and even multiples of 128 and (those that stay for several) with more tiles than workgroups."""
+    import test_gpu_mxfp4 as gpu
+    kinds = ["split1", "split2", "64deep", "64", "128", "256"]
+    names = {"few": "split1", "few of 64 tokens": "split1", "64, 8 stages": "64deep", "64, 4 stages": "64", "128": "128", "256": "256"}
+    assert [p for p, *_ in choose([(1, T, 256, H) for T, H in gpu.TARGETS.values()])] == [names[n] for n in gpu.TARGETS]
+    nan = [(R, T, 384, H) for R, T, H in gpu.NAN_SHAPES]
+    assert {p for p, *_ in choose(nan)} >= set(kinds) - {"split2"}
+    exact = gpu.PRODUCTS + gpu.SMALL_TILES + gpu.LARGE_TILES + gpu.TWO_ROUNDS
+    got = choose(exact)
+    assert {p for p, *_ in got} == set(kinds)
+    assert {l for _, l, *_ in got} == set(kinds) | {"quantize0", "quantize1", "quantize2"}
+    # tiles and workgroups of a round on 256 units: (edge, workgroups a unit)
+    for kind, (edge, per_unit) in {"64": (64, 2), "128": (128, 1), "256": (256, 1)}.items():
+        again = [s for s, g in zip(exact, got) if g[0] == kind
+                 and s[0] * -(-s[1] // edge) * -(-s[3] // edge) > 256 * per_unit]
+        stages = {(-(-K // 128) + 1) // 2 for _, _, K, _ in again}
+        assert {-(-K // 128) % 2 for _, _, K, _ in again} == {0, 1}, kind
+        assert min(stages) == 1 and {s % 2 for s in stages} == {0, 1}, (kind, stages)
+    for kind in kinds:
+        assert {-(-K // 128) % 2 for (_, _, K, _), g in zip(exact, got) if g[0] == kind} == {0, 1}, kind
