@@ -329,3 +329,97 @@ def test_more_rows_than_a_grid_row():
     _say("norm 2^20 + 5 rows")
     _sampled(T, 8, [0, 1, (1 << 20) - 1, 1 << 20, T - 1], F16)
     _sampled(T, 20, [3, (1 << 20) - 1, 1 << 20, T - 1], BF16)
+
+
+# two vectors a thread: rows of 1025 to 2048 vectors, and from 2^23 elements on rows of more than 64; whole
+# rows, rows that end inside a vector, groups of whole vectors and (146, 10: also inside one) of pairs
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("T,H", [(1777, 5003), (5, 8193), (5, 16383), (3, 8207), (16200, 519), (8400, 1001)])
+def test_two_vectors_a_thread(T, H, dt):
+    _say(f"norm, two vectors, T={T} H={H} {dt}")
+    d = _inputs(T, H, dt, 1, H)
+    h, y = Guarded(T, H, dt), Guarded(T, H, dt)
+    fc.fc_residual_norm(**_cuda(d), gate_tokens=1, eps=EPS, res_scale=1.25, out_scale=-0.5, h=h.t, y=y.t)
+    torch.cuda.synchronize()
+    _check(h.t, y.t, _f64(d), 1, dt, 1.25, -0.5)
+    h.check()
+    y.check()
+
+
+def _payload(T, H, bits, group, seed):
+    g = torch.Generator().manual_seed(seed)
+    codes = torch.randint(0, 256, (T, H * bits // 8), generator=g, dtype=torch.uint8)
+    s = (torch.rand((T, H // group), generator=g) * 0.3).half()
+    z = torch.randn((T, H // group), generator=g).half()
+    return codes, s, z
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("T,H,bits,group", [
+    (1100, 8192, 4, 128), (1030, 8192, 8, 128), (1900, 4608, 8, 96), (1900, 4608, 4, 96), (3, 12288, 4, 96), (2, 16384, 8, 16384),
+    (3, 10010, 4, 10), (3, 10010, 8, 10), (900, 10010, 4, 10), (900, 10010, 8, 2), (2, 16382, 4, 16382), (840, 10074, 4, 146),
+    (15000, 576, 4, 36)])
+def test_payload_two_vectors_a_thread(T, H, bits, group, dt):
+    _say(f"wire norm, two vectors, T={T} H={H} int{bits} g{group} {dt}")
+    d = _inputs(T, H, dt, 3, T + H + bits)
+    codes, s, z = _payload(T, H, bits, group, H)
+    d["x"] = ref.dequantize(codes, s, z, bits, group)
+    h, y = Guarded(T, H, dt), Guarded(T, H, dt)
+    c = _cuda({k: v for k, v in d.items() if k != "x"})
+    fc.fc_dequantize_residual_norm(codes.cuda(), s.view(torch.uint16).cuda(), z.view(torch.uint16).cuda(), T, H, bits,
+                                   group, **c, gate_tokens=3, eps=EPS, res_scale=1.25, out_scale=0.5, h=h.t, y=y.t)
+    torch.cuda.synchronize()
+    _check(h.t, y.t, _f64(d), 3, dt, 1.25, 0.5)
+    h.check()
+    y.check()
+
+
+@pytest.mark.parametrize("T,H,bits,group,pre", [(8200, 8192, 4, 128, True), (4200, 16382, 8, 2, True), (16500, 8192, 4, 128, False)])
+def test_payload_outputs_past_the_cache(T, H, bits, group, pre):
+    """Outputs of more than 256 MiB, with y and h alone; sampled rows."""
+    _say(f"wire norm past the cache T={T} H={H} int{bits} g{group}")
+    g = torch.Generator(device="cuda").manual_seed(T)
+    codes = torch.randint(0, 256, (T, H * bits // 8), generator=g, device="cuda", dtype=torch.uint8)
+    s = (torch.rand((T, H // group), generator=g, device="cuda") * 0.3).half()
+    z = torch.randn((T, H // group), generator=g, device="cuda").half()
+    res = torch.randn((T, H), generator=g, device="cuda").to(BF16)
+    w = (1 + 0.2 * torch.randn(H, generator=g, device="cuda")).to(BF16)
+    h, y = Guarded(T, H, BF16), Guarded(T, H, BF16)
+    fc.fc_dequantize_residual_norm(codes, s.view(torch.uint16), z.view(torch.uint16), T, H, bits, group, res, w_post=w,
+                                   w_pre=w if pre else None, eps=EPS, h=h.t, y=y.t if pre else None)
+    torch.cuda.synchronize()
+    h.check()
+    y.check()
+    at = torch.tensor([0, 1, 511, T // 2, T - 2, T - 1])
+    wd = w.cpu().double()
+    d = dict(x=ref.dequantize(codes[at].cpu(), s[at].cpu(), z[at].cpu(), bits, group), residual=res[at].cpu().double(),
+             w_post=wd, gate=None, w_pre=wd if pre else None)
+    _check(h.t[at], y.t[at] if pre else None, d, 1, BF16, 1.0, 1.0)
+    if not pre:
+        assert (y.raw == 0x5A5A).all()
+
+
+@pytest.mark.parametrize("T,H", [(700, 9), (700, 515), (600, 1001), (500, 5003), (300, 8193), (100, 20001), (200, 32770), (60, 65535)])
+def test_in_place_rows_that_end_inside_a_vector(T, H):
+    """The load of such a row's last vector overlaps elements that other threads own and, in place,
+    overwrite: the outputs are those of the call out of place."""
+    _say(f"norm in place T={T} H={H}")
+    d = _cuda(_inputs(T, H, F16, 1, H))
+    h, y = fc.fc_residual_norm(**d)
+    stream = d["residual"].clone()
+    h2, y2 = fc.fc_residual_norm(**dict(d, residual=stream), h=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(h, stream) and torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("T,H,bits,group", [(500, 10010, 4, 10), (300, 32770, 8, 290), (64, 65534, 4, 2), (1100, 8192, 4, 128)])
+def test_payload_in_place(T, H, bits, group):
+    _say(f"wire norm in place T={T} H={H} int{bits} g{group}")
+    d = _cuda({k: v for k, v in _inputs(T, H, BF16, 1, H).items() if k != "x"})
+    codes, s, z = _payload(T, H, bits, group, T)
+    p = (codes.cuda(), s.view(torch.uint16).cuda(), z.view(torch.uint16).cuda(), T, H, bits, group)
+    h, y = fc.fc_dequantize_residual_norm(*p, **d)
+    stream = d["residual"].clone()
+    h2, y2 = fc.fc_dequantize_residual_norm(*p, **dict(d, residual=stream), h=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(h, stream) and torch.equal(y, y2)
