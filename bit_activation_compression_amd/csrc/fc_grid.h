@@ -1,4 +1,5 @@
-// Grids of the layer operators (include/fc/layer.h).
+// Grids: the device's compute units, and rows of workgroups for the layer
+// operators (include/fc/layer.h).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -21,8 +22,9 @@ inline dim3 grid_of_blocks(uint64_t blocks) {
     return blocks <= row ? dim3((unsigned)blocks) : dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
 }
 
-// Compute units of the current device, looked up once per device (atomic:
-// host threads may fill the cache at once, with the same value).
+// Compute units of the current device (persistent kernels have a workgroup or
+// two on each), looked up once per device. The cache is atomic: calls from
+// several host threads may fill it at once (with the same value).
 inline int compute_units() {
     static std::atomic<int> cached[64] = {};
     int dev = 0;

@@ -48,10 +48,10 @@
 //     in a 256-byte LDS sink): the staging loads then hit L2 instead of
 //     waiting on the Infinity Cache or HBM, which the workgroup barrier of
 //     every pair would otherwise wait for.
-#include <atomic>
 #include <type_traits>
 
 #include "fc_device.h"
+#include "fc_grid.h"
 #include "fc_launch.h"
 
 namespace fc {
@@ -642,23 +642,6 @@ void linear_quantize_kernel(
         if (KP > 1) pair_in(nxt, 1);
         cur = nxt;
     }
-}
-
-// Compute units of the current device (one persistent workgroup each),
-// looked up once per device. The cache is atomic: calls from several host
-// threads may fill it at once (with the same value).
-int compute_units() {
-    static std::atomic<int> cached[64] = {};
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return -1;
-    int n = cached[dev].load(std::memory_order_relaxed);
-    if (n <= 0) {
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-            n <= 0)
-            return -1;
-        cached[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
 }
 
 // order: 1 the XCD-grid tile order, 0 the XCD runs, -1 the grid exactly when

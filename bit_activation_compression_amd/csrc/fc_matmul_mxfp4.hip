@@ -70,12 +70,10 @@ namespace fc {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 // stores at the alignment of one output
 typedef u32x2 u32x2_u16 __attribute__((aligned(2)));
 typedef uint32_t u32_u16 __attribute__((aligned(2)));
 
-constexpr int kFp4 = 4;                   // operand format of the f8f6f4 instructions
 constexpr int kStageBytes = 128;          // bytes of codes of a row in a stage
 constexpr int kStageScales = 8;           // bytes of scales
 constexpr int kStageSteps = 4;
@@ -88,19 +86,14 @@ constexpr int kPrefetchTiles = 4;         // tiles per compute unit from which i
 constexpr int kShareA = 8;                // channel tiles among which a token tile's prefetch is shared
 constexpr int kXcds = 8;
 constexpr int kLdsBytes = 160 * 1024;     // LDS of a compute unit
-constexpr uint32_t kPast = 0xFFFFFFF0u;   // an offset past every resource
-// buffer resource word 3 for raw (untyped, unswizzled) 32-bit-addressed
-// buffers on gfx9-family GPUs
-constexpr int kRawBufferFlags = 0x00020000;
 constexpr int kNonTemporal = 2;           // cache policy of a buffer store
 
 // SEL: byte of both scale words (0 or 2)
 template <int SEL>
 __device__ __forceinline__ f32x16 mfma_mx(const u32x4 &w, const u32x4 &a, const f32x16 &c, uint32_t sw,
                                           uint32_t sa) {
-    const i32x8 wv = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
-    const i32x8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, av, c, kFp4, kFp4, SEL, (int)sw, SEL, (int)sa);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(w), mx_operand(a), c, kFp4, kFp4, SEL, (int)sw,
+                                                           SEL, (int)sa);
 }
 
 // s_waitcnt until at most N vector-memory operations of this wave are

@@ -28,13 +28,9 @@ namespace fc {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kFp4 = 4;
 constexpr int kStepBytes = 64;            // codes of a row in a step
 constexpr int kStepScales = 4;
-constexpr uint32_t kPast = 0xFFFFFFF0u;
-constexpr int kRawBufferFlags = 0x00020000;
 constexpr int kLdsPad = 16;               // spreads the token rows over the banks
 
 struct FewArgs {
@@ -49,9 +45,8 @@ struct FewArgs {
 
 __device__ __forceinline__ f32x4 mfma_mx(const u32x4 &w, const u32x4 &a, const f32x4 &c, uint32_t sw,
                                          uint32_t sa) {
-    const i32x8 wv = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
-    const i32x8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, av, c, kFp4, kFp4, 0, (int)sw, 0, (int)sa);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(w), mx_operand(a), c, kFp4, kFp4, 0, (int)sw, 0,
+                                                            (int)sa);
 }
 
 __device__ __forceinline__ u32x4 buffer16(const __amdgpu_buffer_rsrc_t &r, uint32_t off) {

@@ -10,6 +10,18 @@ namespace fc {
 constexpr int kMxBlockElems = 32;   // values per scale
 constexpr int kMxStepElems = 128;   // rows are padded to a multiple of this
 
+// --- the scaled matrix cores (v_mfma_scale_f32_*_f8f6f4) ---
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+constexpr int kFp4 = 4;                   // operand format
+// a lane's 32 FP4 codes as the instruction's operand of up to 8 bits a value
+__device__ __forceinline__ i32x8 mx_operand(const u32x4 &v) {
+    return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+}
+// buffer resource word 3 for raw (untyped, unswizzled) 32-bit-addressed
+// buffers on gfx9-family GPUs
+constexpr int kRawBufferFlags = 0x00020000;
+constexpr uint32_t kPast = 0xFFFFFFF0u;   // an offset past every resource
+
 // 8 elements of 16 bits at the alignment of one (one global_load_dwordx4)
 typedef u32x4 u32x4_u16 __attribute__((aligned(2)));
 
