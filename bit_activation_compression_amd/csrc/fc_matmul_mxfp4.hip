@@ -586,7 +586,6 @@ hipError_t by_shape(const MxArgs &p, int R, int cus, hipStream_t stream) {
     case Mxfp4Tile::k256: return launch_tiles<DT, 256, 256, 2, 4, 2, false>(p, R, cus, stream);
     case Mxfp4Tile::k128: return launch_tiles<DT, 128, 128, 2, 2, 4, false>(p, R, cus, stream);
     case Mxfp4Tile::k64: return launch_tiles<DT, 64, 64, 2, 2, 4, true>(p, R, cus, stream);
-    case Mxfp4Tile::k64Deep: return launch_tiles<DT, 64, 64, 2, 2, 8, true>(p, R, cus, stream);
     }
     return hipErrorInvalidConfiguration;
 }

@@ -14,7 +14,7 @@ int main() {
     while (scanf("%d %d %d %d", &R, &T, &K, &H) == 4) {
         const int Kp = (K + 127) / 128 * 128, steps = Kp / 128;
         const int rounds = mxfp4_split_rounds(R, H, steps, cus);
-        const char *const tile[] = {"256", "128", "64", "64deep"};
+        const char *const tile[] = {"256", "128", "64"};
         char product[32], linear[32];
         if (mxfp4_few_tokens(R, T, steps, H, cus)) snprintf(product, sizeof product, "split%d", rounds);
         else snprintf(product, sizeof product, "%s", tile[(int)mxfp4_tile(R, T, H, cus)]);

@@ -464,9 +464,9 @@ def test_product_of_the_most_tokens():
     torch.cuda.empty_cache()
 
 
-# one shape for each kernel of the product on 256 compute units, but for the many-tile ones
-TARGETS = {"few": (1, 64), "few of 64 tokens": (64, 64), "64, 8 stages": (300, 512), "64, 4 stages": (1408, 3200),
-           "128": (1024, 4096), "256": (2176, 4096)}
+# one shape (T, K, H) for each kernel of the product on 256 compute units, but for the many-tile ones
+TARGETS = {"split1 of 1 token": (1, 256, 64), "split1 of 32 tokens": (32, 256, 64), "split1 of 64 tokens": (64, 4096, 64),
+           "64": (300, 256, 512), "64 in two rounds": (1408, 256, 3200), "128": (1024, 256, 4096), "256": (2176, 256, 4096)}
 
 
 @pytest.mark.parametrize("target", TARGETS)
@@ -474,7 +474,7 @@ def test_small_scales(target):
     """Exponents that sum to e: sums are multiples of 2^(e - 2), which binary32 holds, among them
     subnormal ones, and one rounding takes them to bf16's subnormals. With both scales 2^-127 every
     sum is far below 2^-149: zeros."""
-    (T, H), K = TARGETS[target], 256
+    T, K, H = TARGETS[target]
     ac, as_, wc, ws = _operands(1, T, K, H, 5, 0)
     as_[...] = 0
     for e in (-125, -135, -140, -254):
@@ -491,7 +491,7 @@ def test_small_scales(target):
 @pytest.mark.parametrize("a_byte,w_byte", [(0, 247), (247, 0), (254, 0), (0, 254), (254, 1)])
 def test_extreme_scales_in_every_kernel(target, a_byte, w_byte):
     """Neither scale alone leaves a product in binary32's range."""
-    (T, H), K = TARGETS[target], 256
+    T, K, H = TARGETS[target]
     _say(f"extreme scales {target} {a_byte} {w_byte}")
     ac, as_, wc, ws = _operands(1, T, K, H, 6, 0)
     as_[...] = a_byte
@@ -506,8 +506,8 @@ NAN_SHAPES = [(1, 1, 64), (1, 50, 64), (1, 64, 130), (1, 300, 512), (1, 1408, 32
               (1, 2176, 4096), (2, 1000, 4360), (8, 2900, 2900)]
 
 
-@pytest.mark.parametrize("K", [128, 384, 512, 640, 1152])
-@pytest.mark.parametrize("R,T,H", NAN_SHAPES)
+@pytest.mark.parametrize("R,T,H,K", [(*s, K) for s in NAN_SHAPES for K in (128, 384, 512, 640, 1152)]
+                         + [(1, 50, 64, 4096), (1, 64, 130, 4224), (1, 2, 4200, 4224), (2, 16, 2100, 8192)])
 def test_nan_scales_in_every_kernel(R, T, H, K):
     """NaN scales in the first and the last block of rows at the tiles' borders make those rows (of a)
     and channels (of w) NaN and no other: the row before one whose first scale is NaN ends in the
@@ -567,7 +567,7 @@ def test_nan_activations_quantized_in_place(T, K, H):
 SMALL_TILES = [(1, 1408, 128, 3200), (1, 1408, 384, 3200), (1, 1350, 1000, 3230), (1, 1390, 1280, 3137), (4, 40, 384, 8300),
                (4, 64, 896, 8257), (9, 3, 256, 4100), (9, 50, 640, 4101), (3, 17, 1408, 12000)]
 LARGE_TILES = [(2, 2300, 512, 1700), (2, 2300, 1280, 1702), (8, 1300, 512, 2100), (8, 1300, 384, 2101)]
-TWO_ROUNDS = [(1, 1, 4096, 4200), (1, 3, 4100, 8192), (2, 16, 4224, 2100), (1, 17, 4096, 4097), (1, 24, 4352, 8191), (2, 20, 4100, 4096)]
+TWO_ROUNDS = [(1, 1, 4096, 4200), (1, 3, 4100, 8192), (2, 16, 8320, 2100), (1, 13, 8192, 4097), (1, 24, 4352, 8191), (2, 20, 4100, 4096)]
 
 
 @pytest.mark.parametrize("dt", [BF16, F16])
