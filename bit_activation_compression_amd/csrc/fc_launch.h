@@ -82,9 +82,7 @@ struct NormArgs {
     float res_scale, out_scale, eps, inv_h;
     uint16_t *h, *y;
     int T, H;
-    // set by the launchers, see fc_norm.h
-    int waves;            // of a workgroup
-    bool past_cache;      // h and y do not fit the Infinity Cache
+    int waves;            // of a workgroup (set by the launchers, see fc_norm.h)
 };
 hipError_t launch_residual_norm(const NormArgs &a, int dtype, hipStream_t stream);
 hipError_t launch_dequantize_residual_norm(const NormArgs &a, int dtype, int bits, int group,

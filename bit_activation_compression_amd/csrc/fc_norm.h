@@ -17,11 +17,14 @@
 // all the same), and the last vector of a row that is no whole number of them
 // loads the row's last 8 elements.
 //
-// Measured: 8192 rows of 4096 (fp16, post-norm) 39.3 us, 6.8 TB/s; 8192 rows of
-// 8192 from an INT4 payload 76 us, 5.7 TB/s; 1777 rows of 5003 with a gate per
-// token 18.3 us, 4.9 TB/s. One row is a launch and two reductions: 3.7 us.
-// Non-temporal loads were slower, and so was shifting the vectors of a
-// misaligned row to whole 16-byte ones (28 against 18.3 us).
+// Measured: 8192 rows of 4096 (fp16, post-norm) 48 us, 5.6 TB/s (on one set of
+// buffers, part of which the Infinity Cache then holds, 39.4); 8192 rows of 8192 from
+// an INT4 payload 76 us, 5.7 TB/s; 1777 rows of 5003 with a gate per token 18.3 us,
+// 4.9 TB/s. One row is a launch and two reductions: 3.7 us. Non-temporal loads
+// were slower, and so was shifting the vectors of a misaligned row to whole 16-byte
+// ones (28 against 18.3 us). Non-temporal stores change nothing: 8192 x 8192 from an
+// INT4 payload 75.8 against 76.0, 8192 x 8192 94.4 against 94.4, 65536 x 1024 92.7
+// against 92.5, 4096 x 32768 213.8 against 212.3.
 #pragma once
 
 #include "fc_device.h"
@@ -33,7 +36,6 @@ namespace {
 
 constexpr int kNormThreads = 1024;   // most of a workgroup
 constexpr uint64_t kManyElems = uint64_t(1) << 23;
-constexpr uint64_t kInfinityCache = uint64_t(256) << 20;
 
 // vectors at the alignment of their elements
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
@@ -99,12 +101,9 @@ __device__ __forceinline__ u32x4 load_row8(const uint16_t *row, int b, int H) {
 
 // v[k] is element b + k; the lane's own are those from e to the row's end.
 template <int DT>
-__device__ __forceinline__ void store_row8(uint16_t *row, int e, int b, int H, bool past_cache,
-                                           const float (&v)[kLaneElems]) {
+__device__ __forceinline__ void store_row8(uint16_t *row, int e, int b, int H, const float (&v)[kLaneElems]) {
     if (e + kLaneElems <= H) {
-        u32x4_a2 *p = reinterpret_cast<u32x4_a2 *>(row + e);
-        if (past_cache) __builtin_nontemporal_store(narrow8<DT>(v), p);
-        else *p = narrow8<DT>(v);
+        *reinterpret_cast<u32x4_a2 *>(row + e) = narrow8<DT>(v);
         return;
     }
 #pragma unroll
@@ -277,7 +276,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormArgs a) {
         own(v, x[v]);
 #pragma unroll
         for (int k = 0; k < kLaneElems; ++k) ss = __builtin_fmaf(x[v][k], x[v][k], ss);
-        store_row8<DT>(hrow, elem(v), begin(v), H, a.past_cache, x[v]);
+        store_row8<DT>(hrow, elem(v), begin(v), H, x[v]);
     }
     if (a.w_pre == nullptr) return;
     const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(block_sum(ss, part[1], (uint32_t)a.waves), a.inv_h, a.eps));
@@ -288,7 +287,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(const NormArgs a) {
         widen8<DT>(operand(wpre, a.w_pre, v), w);
 #pragma unroll
         for (int k = 0; k < kLaneElems; ++k) w[k] *= x[v][k] * rstd;
-        store_row8<DT>(yrow, elem(v), begin(v), H, a.past_cache, w);
+        store_row8<DT>(yrow, elem(v), begin(v), H, w);
     }
 }
 
@@ -303,15 +302,12 @@ hipError_t launch_norm_rows(NormArgs a, int nv, hipStream_t stream) {
 template <int DT, int SRC, bool GEN>
 hipError_t launch_norm_any(NormArgs a, hipStream_t stream) {
     const int nv = (a.H + kLaneElems - 1) / kLaneElems;   // vectors of a row
-    // Outputs that the Infinity Cache cannot hold for their readers are written
-    // past it: 8192 x 8192 from an INT4 payload 79 -> 76 us, 4096 x 16384 99 -> 95;
-    // outputs that fit it are faster through it (8192 x 4096: 43 against 48).
-    a.past_cache = (uint64_t)a.T * (uint64_t)a.H * (a.y ? 4 : 2) > kInfinityCache;
-    // Two vectors per thread once the device is full of rows: H = 8192 bf16,
-    // 512 / 1024 / 2048 rows 9.2 / 12.7 / 24.1 us against 9.0 / 14.2 / 24.6 with
-    // one; H = 4096, 512 / 1024 / 8192 rows 5.6 / 9.0 / 43.0 against 5.5 / 8.7 / 44.5.
-    // Rows of at most a wave's 64 vectors would leave half of it idle with two (30000
-    // rows of 256: 23.6 against 13.2).
+    // Two vectors per thread once the device is full of rows, us with one / two (bf16,
+    // in a graph on buffers that the caches do not hold): H = 8192, 512 / 1024 / 2048 /
+    // 8192 rows 9.2 / 17.0 / 29.4 / 98.0 against 9.4 / 15.7 / 27.0 / 95.2; H = 4096, 512 /
+    // 1024 / 8192 rows 6.0 / 9.1 / 48.2 against 6.1 / 9.4 / 48.4. Rows of at most a wave's
+    // 64 vectors would leave half of it idle with two (30000 rows of 256: 23.6 against
+    // 13.2 on one set of buffers).
     const bool few = nv <= kWave || (uint64_t)a.T * (uint64_t)a.H < kManyElems;
     if (nv <= kNormThreads && few) return launch_norm_rows<DT, SRC, GEN, 1>(a, nv, stream);
     if (nv <= 2 * kNormThreads) return launch_norm_rows<DT, SRC, GEN, 2>(a, nv, stream);
