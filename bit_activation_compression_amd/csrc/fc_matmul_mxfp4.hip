@@ -30,9 +30,11 @@
 //     channels of a token and 32 lanes 64 NH bytes of it. With channels as rows,
 //     where a store has 32 bytes of each of 32 tokens, 70B o_proj slices take 338 us
 //     for 297 and 4 x 1024 tokens, K = 3584, H = 4096 39 for 36. Outputs of 128 MiB
-//     and more are stored past the caches (321 -> 297; 2 ranks of 4096 x 4096 x 4096,
-//     64 MiB, 72.3 against 73.5 so). Tiles of 64 have one block: the rows are channels
-//     and two lanes have 32 bytes of a token;
+//     and more are stored past the caches (321 -> 297). Near that size it is so and so:
+//     on operands that the Infinity Cache holds it loses (64 MiB, 2 ranks of 4096 x 4096
+//     x 4096, 72.5 -> 75.8; 128 MiB, 8 ranks of 2048 x 1024 x 4096, 49.3 -> 53.7), on
+//     others it gains (75.7 -> 75.7; 56.1 -> 53.0). Tiles of 64 have one block: the
+//     rows are channels and two lanes have 32 bytes of a token;
 //   - rows past H or T lie past the buffer resources and read as zeros. Where K
 //     is an odd multiple of 128, the second half of the last stage is not
 //     fetched (zeros again) and gets scales of 0;
@@ -41,8 +43,9 @@
 //     share of the next two stages' lines, in the place of every other scale
 //     load, which has nothing to fetch. Two stages in LDS do not cover the way
 //     past the L2: 70B d_proj slices 980 -> 924 us, 8192 x 8192 x 8192 270 ->
-//     257. Calls of fewer than 4 tiles per compute unit (whose operands the first
-//     tiles bring into the L2) lose: 2 ranks of 4096 x 4096 x 4096 74 -> 77;
+//     257. Calls of fewer than 4 tiles per compute unit lose on operands that the
+//     Infinity Cache holds (2 ranks of 4096 x 4096 x 4096 76.0 -> 78.6; 1 rank of 8192 x
+//     4096 x 4096 72.6 -> 74.6) and gain on others (82.7 -> 77.9; 80.6 -> 77.2);
 //   - workgroups are persistent: stages of consecutive tiles form one stream,
 //     so the next tile's first stages are in flight during a tile's epilogue.
 //     The tiles are split into one contiguous run per XCD (workgroup b runs on
@@ -50,7 +53,7 @@
 //     workgroups of an XCD share operands in its L2.
 //
 // What bounds it: the 70B d_proj slices (R = 4, T = 8192, K = 7168, H = 8192)
-// take 0.92 ms, 4.2 PFLOP/s. The large tile's matrix instructions alone run at
+// take 0.91 to 0.93 ms, 4.1 to 4.2 PFLOP/s. The large tile's matrix instructions alone run at
 // 5.3 PFLOP/s with all compute units on random operands (9.8 without the
 // toggling: the power management lowers the clock). With everything else the
 // clock is 1.6 to 1.7 GHz and the matrix cores are busy 60% of the cycles: a

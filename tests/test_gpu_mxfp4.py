@@ -597,3 +597,46 @@ def test_product_and_linear_in_every_kernel(R, T, K, H, dt):
     a = ref.mx_dequantize(*ref.mx_quantize(x.double()), K).float()
     for r in range(R):
         assert torch.equal(y[r].cpu(), (a[r] @ w[r].t().contiguous()).to(dt)), f"rank {r}"
+
+
+def test_host_threads_on_streams_of_their_own():
+    """Four threads at once, each on its stream with tensors of its own: the chain of norms, quantizing
+    linear layers (few tokens and tiles) and the all-reduce gives what it gives alone."""
+    import threading
+
+    R, K, H = 2, 1024, 2048
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda").to(BF16)
+    wc, ws = fc.fc_quantize_mxfp4(n(R, H, K))
+    gain = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(BF16)
+
+    def chain(a, res, stream=None):
+        y = fc.fc_linear_mxfp4(a, wc, ws, stream=stream)
+        h, v, _ = fc.fc_allreduce_emulated_norm(y, 4, 128, res, w_post=gain, w_pre=gain, stream=stream)
+        h2, v2 = fc.fc_residual_norm(v, h, w_pre=gain, stream=stream)
+        codes, scales = fc.fc_quantize_mxfp4(v2, stream=stream)
+        return y, h, v, h2, v2, fc.fc_dequantize_mxfp4(codes, scales, H, BF16, stream=stream)
+
+    inputs = [(n(R, T, K), n(T, H)) for T in (1, 5, 200, 700)]
+    want = [chain(*i) for i in inputs]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(inputs), []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(20):
+                got[i] = chain(*inputs[i], stream=stream)
+            stream.synchronize()
+        except Exception as e:     # reported by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(inputs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
