@@ -1,7 +1,7 @@
 """Low-bit all-reduce activation codec for AMD Instinct MI355X (gfx950).
 
-A thin ctypes binding over the C ABI in `include/fc.h` and `include/fc/layer.h`
-(libfc.so, built from `csrc/` by `build.py`). Every step of the codec runs in the library's HIP
+A thin ctypes binding over the C ABI in `include/fc.h`, `include/fc/layer.h` and
+`include/fc/train.h` (libfc.so, built from `csrc/` by `build.py`). Every step of the codec runs in the library's HIP
 kernels; this module only checks tensor metadata, allocates outputs with
 torch on the input's device, and passes raw device pointers and the current
 HIP stream. There is no fallback: if the library cannot be loaded, calls
@@ -30,6 +30,10 @@ __all__ = [
     "fc_residual_norm", "fc_dequantize_residual_norm", "fc_allreduce_emulated_norm",
     "fc_quantize_mxfp4", "fc_dequantize_mxfp4", "fc_matmul_mxfp4", "fc_linear_mxfp4",
     "fc_linear_mxfp4_workspace_bytes", "LAYER_SYMBOLS",
+    "fc_layer_norm", "fc_layer_norm_backward", "fc_linear_act", "fc_linear_input_grad",
+    "fc_linear_weight_grad", "fc_activation_backward", "fc_layer_norm_backward_workspace_bytes",
+    "fc_linear_weight_grad_workspace_bytes", "fc_activation_backward_workspace_bytes", "ACTIVATIONS",
+    "TRAIN_SYMBOLS",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -51,6 +55,12 @@ LAYER_SYMBOLS = (
     "fc_quantize_mxfp4", "fc_dequantize_mxfp4", "fc_matmul_mxfp4", "fc_linear_mxfp4",
     "fc_linear_mxfp4_workspace_bytes",
 )
+TRAIN_SYMBOLS = (
+    "fc_layer_norm", "fc_layer_norm_backward", "fc_linear_act", "fc_linear_input_grad",
+    "fc_linear_weight_grad", "fc_activation_backward", "fc_layer_norm_backward_workspace_bytes",
+    "fc_linear_weight_grad_workspace_bytes", "fc_activation_backward_workspace_bytes",
+)
+ACTIVATIONS = ("none", "relu", "silu", "gelu", "gelu_tanh")   # their places are the C ABI's fc_act
 # FC_NOALLOC_SCRATCH_BYTES of include/fc.h: the payload scratch the library holds per device
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -107,6 +117,21 @@ def lib() -> ctypes.CDLL:
                 f.restype = I
             L.fc_linear_mxfp4_workspace_bytes.argtypes = [I, I, I]
             L.fc_linear_mxfp4_workspace_bytes.restype = Z
+            L.fc_layer_norm.argtypes = [P, I, I, I, P, P, F, I, P, P, P, P, P, P, I, P]
+            L.fc_layer_norm_backward.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P, P, P, P, P, P, Z, P]
+            L.fc_linear_act.argtypes = [P, P, I, I, I, I, I, P, I, P, P, P, P, P]
+            L.fc_linear_input_grad.argtypes = [P, P, I, I, I, I, I, P, P, P]
+            L.fc_linear_weight_grad.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P, Z, P]
+            L.fc_activation_backward.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, P, Z, P]
+            for f in (L.fc_layer_norm, L.fc_layer_norm_backward, L.fc_linear_act, L.fc_linear_input_grad,
+                      L.fc_linear_weight_grad, L.fc_activation_backward):
+                f.restype = I
+            L.fc_layer_norm_backward_workspace_bytes.argtypes = [I, I]
+            L.fc_linear_weight_grad_workspace_bytes.argtypes = [I, I, I, I]
+            L.fc_activation_backward_workspace_bytes.argtypes = [I, I, I]
+            for f in (L.fc_layer_norm_backward_workspace_bytes, L.fc_linear_weight_grad_workspace_bytes,
+                      L.fc_activation_backward_workspace_bytes):
+                f.restype = Z
             L.fc_workspace_bytes_mixed.argtypes = [I, I, I, I, I, I]
             L.fc_workspace_bytes_mixed.restype = Z
             L.fc_workspace_layout_mixed.argtypes = [I, I, I, I, I, I, ctypes.POINTER(Z),
@@ -683,3 +708,245 @@ def fc_linear_mxfp4(a: torch.Tensor, w_codes, w_scales, y=None, workspace=None, 
         have, pk = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     _launch("fc_linear_mxfp4", dev, stream, a.data_ptr(), pw, pws, _dt(a, "a"), R, T, K, H, py, pk, have)
     return y
+
+
+# --- training through 8-bit activation checkpoints (include/fc/train.h) ------
+
+def _act(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, not {act!r}")
+    return ACTIVATIONS.index(act)
+
+
+def _out(t, name: str, like: torch.Tensor, shape, dtype, stream):
+    """An output: the caller's tensor, checked, or a new one; -> (tensor, address)."""
+    if t is None:
+        t = _empty(like, shape, dtype, stream)
+        return t, t.data_ptr()
+    return t, _like(t, name, tuple(shape), dtype, like.device)
+
+
+def _optional(t, name: str, shape, dtype, device):
+    return None if t is None else _like(t, name, tuple(shape), dtype, device)
+
+
+def _room_for(workspace, need: int, like: torch.Tensor, stream):
+    """A workspace of `need` bytes; -> (what keeps it alive, address, bytes)."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = _empty(like, need, torch.uint8, stream)
+        return workspace, workspace.data_ptr(), need
+    _room(workspace, "workspace", 0, like.device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _saved(payload, name: str, shape, device):
+    """An INT8 payload (codes, s, z) of `shape` -> (the addresses of the three, group)."""
+    codes, s, z = payload
+    lead, H = tuple(shape[:-1]), shape[-1]
+    n = s.shape[-1] if s.dim() else 0
+    if n < 1 or H % n != 0:
+        raise ValueError(f"the rows of {name}s hold {n} groups, those of {name}codes {H} values")
+    return (_like(codes, name + "codes", (*lead, H), torch.uint8, device),
+            _like(s, name + "s", (*lead, n), torch.uint16, device),
+            _like(z, name + "z", (*lead, n), torch.uint16, device), H // n)
+
+
+def fc_layer_norm(x: torch.Tensor, w=None, b=None, eps: float = 1e-5, rms: bool = False, stats: bool = False,
+                  group: int = 0, y=None, mean=None, rstd=None, payload=None, stream=None):
+    """Layer norm of x [T, H] (fp16/bf16), or its RMS norm -> (y, mean, rstd, payload). w and
+    b [H]: weight and bias (None: 1 and 0). stats: mean (None for rms) and rstd, binary32 [T],
+    for the backward pass. group: also the INT8 payload (codes, s, z) of x in groups of that
+    many values, as fc_quantize_groups(x, 8, group) writes it. What is not asked for is None."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    dev, dt = x.device, x.dtype
+    _ints(T=T, H=H, group=group)
+    code = _dt(x, "x")
+    px = _like(x, "x", (T, H), dt, dev)
+    pw, pb = _optional(w, "w", (H,), dt, dev), _optional(b, "b", (H,), dt, dev)
+    y, py = _out(y, "y", x, (T, H), dt, stream)
+    pm = pr = pc = ps = pz = None
+    if mean is not None and rms:
+        raise ValueError("the RMS norm has no mean")
+    if (stats or mean is not None) and not rms:
+        mean, pm = _out(mean, "mean", x, (T,), torch.float32, stream)
+    if stats or rstd is not None:
+        rstd, pr = _out(rstd, "rstd", x, (T,), torch.float32, stream)
+    if payload is not None and not group:
+        raise ValueError("a payload needs its group")
+    if group:
+        if group < 0 or H % group != 0:
+            raise ValueError(f"group must divide H = {H}, not {group}")
+        codes, s, z = payload if payload is not None else (None, None, None)
+        codes, pc = _out(codes, "codes", x, (T, H), torch.uint8, stream)
+        s, ps = _out(s, "s", x, (T, H // group), torch.uint16, stream)
+        z, pz = _out(z, "z", x, (T, H // group), torch.uint16, stream)
+        payload = (codes, s, z)
+    _launch("fc_layer_norm", dev, stream, px, code, T, H, pw, pb, eps, int(rms), py, pm, pr, pc, ps, pz, group)
+    return y, mean, rstd, payload
+
+
+def fc_layer_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    _ints(T=T, H=H)
+    return (_lib or lib()).fc_layer_norm_backward_workspace_bytes(T, H)
+
+
+def fc_layer_norm_backward(dy: torch.Tensor, x, mean, rstd: torch.Tensor, w=None, rms: bool = False,
+                           bias: bool = True, dres=None, dx=None, dw=None, db=None, workspace=None, stream=None):
+    """Backward pass of fc_layer_norm: dy [T, H]; x [T, H] or its payload (codes, s, z); mean
+    (None for rms) and rstd as the forward pass gave them -> (dx, dw, db). dres [T, H] is added
+    to dx (the gradient that the skip connection brings; `dx` may be `dres` or `dy`). dw and db
+    are binary32 [H]: dw where there is a w (or a `dw`), db where `bias` (or a `db`)."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be [T, H]")
+    T, H = dy.shape
+    dev, dt = dy.device, dy.dtype
+    _ints(T=T, H=H)
+    code = _dt(dy, "dy")
+    if rms != (mean is None):
+        raise ValueError("mean goes with the layer norm, not with the RMS norm")
+    pdy = _like(dy, "dy", (T, H), dt, dev)
+    px = pc = ps = pz = None
+    group = 0
+    if isinstance(x, torch.Tensor):
+        px = _like(x, "x", (T, H), dt, dev)
+    else:
+        pc, ps, pz, group = _saved(x, "", (T, H), dev)
+    pm, pr = _optional(mean, "mean", (T,), torch.float32, dev), _like(rstd, "rstd", (T,), torch.float32, dev)
+    pw, pres = _optional(w, "w", (H,), dt, dev), _optional(dres, "dres", (T, H), dt, dev)
+    dx, pdx = _out(dx, "dx", dy, (T, H), dt, stream)
+    pdw = pdb = None
+    if w is not None or dw is not None:
+        dw, pdw = _out(dw, "dw", dy, (H,), torch.float32, stream)
+    if bias or db is not None:
+        db, pdb = _out(db, "db", dy, (H,), torch.float32, stream)
+    need = (_lib or lib()).fc_layer_norm_backward_workspace_bytes(T, H) if pdw or pdb else 0
+    workspace, pk, have = _room_for(workspace, need, dy, stream)
+    _launch("fc_layer_norm_backward", dev, stream, pdy, px, pc, ps, pz, group, code, T, H, pm, pr, pw, pres, pdx, pdw, pdb,
+            pk, have)
+    return dx, dw, db
+
+
+def _product(x: torch.Tensor, w: torch.Tensor, name: str):
+    """(R, T, columns of x, rows of w, columns of w) of x [R, T, .] and w [R, H, K], or both without R."""
+    R, T, n = _rows3(x, name)
+    Rw, H, K = _rows3(w, "w")
+    if R != Rw or x.dim() != w.dim():
+        raise ValueError(f"{name} and w must both be of {R} ranks, or both of none")
+    return R, T, n, H, K
+
+
+def fc_linear_act(a: torch.Tensor, w: torch.Tensor, bias=None, act: str = "none", mul=None, residual=None,
+                  y=None, z=None, stream=None):
+    """a [R, T, K] times w [R, H, K] (or both without R; fp16/bf16) -> (y, z):
+        z = a w^T + bias,  y = act(z) * mul + residual
+    with bias [R, H], mul and residual [R, T, H]. z is rounded and returned where a tensor (or
+    True, to allocate one) is passed, else None. `y` may be `residual`. act: ACTIVATIONS."""
+    R, T, K, H, Kw = _product(a, w, "a")
+    if K != Kw:
+        raise ValueError("a must be [R, T, K] and w [R, H, K]")
+    dev, dt = a.device, a.dtype
+    code = _dt(a, "a")
+    lead = tuple(a.shape[:-2])
+    rows = (*lead, T, H)
+    pa, pw = _like(a, "a", tuple(a.shape), dt, dev), _like(w, "w", tuple(w.shape), dt, dev)
+    pb = _optional(bias, "bias", (*lead, H), dt, dev)
+    pm, pr = _optional(mul, "mul", rows, dt, dev), _optional(residual, "residual", rows, dt, dev)
+    y, py = _out(y, "y", a, rows, dt, stream)
+    pz = None
+    if z is False:
+        z = None
+    elif z is not None:
+        z, pz = _out(None if z is True else z, "z", a, rows, dt, stream)
+    _launch("fc_linear_act", dev, stream, pa, pw, code, R, T, K, H, pb, _act(act), pm, pr, py, pz)
+    return y, z
+
+
+def fc_linear_input_grad(dy: torch.Tensor, w: torch.Tensor, residual=None, dx=None, stream=None):
+    """dy [R, T, H] times w [R, H, K] (or both without R) -> dx [R, T, K] = dy w + residual, the
+    gradient of the layer's input. residual [R, T, K] (None: 0) may be `dx` itself."""
+    R, T, H, Hw, K = _product(dy, w, "dy")
+    if H != Hw:
+        raise ValueError("dy must be [R, T, H] and w [R, H, K]")
+    dev, dt = dy.device, dy.dtype
+    code = _dt(dy, "dy")
+    rows = (*dy.shape[:-1], K)
+    pd, pw = _like(dy, "dy", tuple(dy.shape), dt, dev), _like(w, "w", tuple(w.shape), dt, dev)
+    pr = _optional(residual, "residual", rows, dt, dev)
+    dx, px = _out(dx, "dx", dy, rows, dt, stream)
+    _launch("fc_linear_input_grad", dev, stream, pd, pw, code, R, T, K, H, pr, px)
+    return dx
+
+
+def fc_linear_weight_grad_workspace_bytes(R: int, T: int, K: int, H: int) -> int:
+    _ints(R=R, T=T, K=K, H=H)
+    return (_lib or lib()).fc_linear_weight_grad_workspace_bytes(R, T, K, H)
+
+
+def fc_linear_weight_grad(dy: torch.Tensor, payload, dw=None, accumulate: bool = False, workspace=None, stream=None):
+    """dy [R, T, H] and the INT8 payload (codes, s, z) of the layer's input [R, T, K] (or both
+    without R) -> dw [R, H, K] binary32 = dy^T x, added to `dw` where `accumulate`."""
+    R, T, H = _rows3(dy, "dy")
+    Rx, Tx, K = _rows3(payload[0], "codes")
+    if (R, T) != (Rx, Tx) or dy.dim() != payload[0].dim():
+        raise ValueError("dy must be [R, T, H] and the payload's codes [R, T, K]")
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    dev, dt = dy.device, dy.dtype
+    code = _dt(dy, "dy")
+    pd = _like(dy, "dy", tuple(dy.shape), dt, dev)
+    pc, ps, pz, group = _saved(payload, "", payload[0].shape, dev)
+    dw, pw = _out(dw, "dw", dy, (*dy.shape[:-2], H, K), torch.float32, stream)
+    need = (_lib or lib()).fc_linear_weight_grad_workspace_bytes(R, T, K, H)
+    workspace, pk, have = _room_for(workspace, need, dy, stream)
+    _launch("fc_linear_weight_grad", dev, stream, pd, pc, ps, pz, group, code, R, T, K, H, int(accumulate), pw, pk, have)
+    return dw
+
+
+def fc_activation_backward_workspace_bytes(R: int, T: int, H: int) -> int:
+    _ints(R=R, T=T, H=H)
+    return (_lib or lib()).fc_activation_backward_workspace_bytes(R, T, H)
+
+
+def fc_activation_backward(dy: torch.Tensor, act: str, payload=None, mul=None, bias: bool = False, dz=None, dmul=None,
+                           db=None, workspace=None, stream=None):
+    """dy [R, T, H] (or [T, H]) and the INT8 payload (codes, s, z) of the activation's input
+    z -> (dz, dmul, db): dz = dy * mul * act'(z); dmul = dy * act(z) where `mul`, the payload
+    of the second factor, is given; db = sum over tokens of dz, binary32 [R, H], where `bias`
+    (or a `db`). `dz` may be `dy`. act "none" (without payloads) gives db = sum of dy alone."""
+    R, T, H = _rows3(dy, "dy")
+    dev, dt = dy.device, dy.dtype
+    code = _dt(dy, "dy")
+    kind = _act(act)
+    shape = tuple(dy.shape)
+    pd = _like(dy, "dy", shape, dt, dev)
+    pc = ps = pz = pmc = pms = pmz = pdz = pdm = pdb = None
+    group = 0
+    if kind == 0:
+        if payload is not None or mul is not None or dz is not None or dmul is not None:
+            raise ValueError("act none has no payloads, dz or dmul")
+        if not bias and db is None:
+            raise ValueError("act none gives the bias gradient alone: ask for it")
+    else:
+        if payload is None:
+            raise ValueError(f"act {act} needs the payload of its input")
+        pc, ps, pz, group = _saved(payload, "", shape, dev)
+        dz, pdz = _out(dz, "dz", dy, shape, dt, stream)
+        if mul is not None:
+            pmc, pms, pmz, mgroup = _saved(mul, "mul_", shape, dev)
+            if mgroup != group:
+                raise ValueError(f"mul is in groups of {mgroup}, the payload in groups of {group}")
+            dmul, pdm = _out(dmul, "dmul", dy, shape, dt, stream)
+        elif dmul is not None:
+            raise ValueError("dmul needs mul")
+    need = 0
+    if bias or db is not None:
+        db, pdb = _out(db, "db", dy, (*shape[:-2], H), torch.float32, stream)
+        need = (_lib or lib()).fc_activation_backward_workspace_bytes(R, T, H)
+    workspace, pk, have = _room_for(workspace, need, dy, stream)
+    _launch("fc_activation_backward", dev, stream, pd, pc, ps, pz, pmc, pms, pmz, group, code, R, T, H, kind, pdz, pdm, pdb,
+            pk, have)
+    return dz, dmul, db

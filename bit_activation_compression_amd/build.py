@@ -22,7 +22,10 @@ SOURCES = ["fc_api.hip", "fc_quantize.hip", "fc_dequant_sum_requant.hip", "fc_de
            "fc_sum.hip", "fc_linear_quantize.hip", "fc_allreduce_small.hip", "fc_stream.hip",
            "fc_generic.hip", "fc_residual_norm.hip", "fc_dequantize_residual_norm.hip",
            "fc_mxfp4.hip", "fc_matmul_mxfp4.hip",
-           "fc_matmul_mxfp4_few.hip"]
+           "fc_matmul_mxfp4_few.hip",
+           "fc_train_api.hip", "fc_layer_norm.hip", "fc_layer_norm_backward.hip",
+           "fc_activation_backward.hip", "fc_linear_act.hip", "fc_linear_input_grad.hip",
+           "fc_linear_weight_grad.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

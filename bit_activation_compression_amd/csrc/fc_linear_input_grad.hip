@@ -1,0 +1,34 @@
+// The gradient of a linear layer's input, dx = dy w (include/fc/train.h,
+// fc_linear_input_grad): the weights [H][K] are read down their columns. The kernel
+// is in fc_product.h.
+#include "fc_product.h"
+
+namespace fc {
+namespace {
+
+template <int DT>
+hipError_t run(const ProductArgs &a, hipStream_t stream) {
+    if (a.K % kChunk == 0 && a.N % kChunk == 0)
+        return launch_product<DT, kRows, kCols, 128, 128, 2, 2, true, false>(a, stream);
+    return launch_product<DT, kRows, kCols, 128, 128, 2, 2, false, false>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_linear_input_grad(const uint16_t *dy, const uint16_t *w, int dtype, int R, int T, int K,
+                                    int H, const uint16_t *residual, uint16_t *dx, hipStream_t stream) {
+    ProductArgs p = {};
+    p.a = dy;
+    p.b = w;
+    p.R = R;
+    p.M = T;
+    p.N = K;
+    p.K = H;
+    p.split = 1;
+    p.split_k = H;
+    p.e.residual = residual;
+    p.e.y = dx;
+    return dtype == 0 ? run<0>(p, stream) : run<1>(p, stream);
+}
+
+}  // namespace fc
