@@ -89,11 +89,10 @@ hipError_t launch_linear_act(const uint16_t *a, const uint16_t *w, int dtype, in
 // dx[r] = dy[r] w[r] (+ residual): dy [R][T][H], w [R][H][K], dx and residual [R][T][K]
 hipError_t launch_linear_input_grad(const uint16_t *dy, const uint16_t *w, int dtype, int R, int T, int K,
                                     int H, const uint16_t *residual, uint16_t *dx, hipStream_t stream);
-// dw[r] (+)= dy[r]^T x[r] for x a payload [R][T][K]; part: binary32
-// [weight_grad_splits][R][H][K] where that is more than 1
-int weight_grad_splits(int R, int T, int K, int H);
+// dw[r] (+)= dy[r]^T x[r] for x a payload [R][T][K]; workspace as weight_grad_plan
+// (fc_product_dispatch.h) has it
 hipError_t launch_linear_weight_grad(const uint16_t *dy, const Payload &px, int group, int dtype, int R,
-                                     int T, int K, int H, int accumulate, float *dw, float *part,
+                                     int T, int K, int H, int accumulate, float *dw, void *workspace,
                                      hipStream_t stream);
 
 }  // namespace fc

@@ -8,8 +8,8 @@ namespace {
 
 template <int DT>
 hipError_t run(const ProductArgs &a, hipStream_t stream) {
-    if (a.K % kChunk == 0) return launch_product<DT, kRows, kRows, 128, 128, 2, 2, true, false>(a, stream);
-    return launch_product<DT, kRows, kRows, 128, 128, 2, 2, false, false>(a, stream);
+    if (a.K % kChunk == 0) return launch_tiles<DT, kRows, kRows, true, false>(a, stream);
+    return launch_tiles<DT, kRows, kRows, false, false>(a, stream);
 }
 
 }  // namespace

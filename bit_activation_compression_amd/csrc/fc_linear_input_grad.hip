@@ -9,8 +9,8 @@ namespace {
 template <int DT>
 hipError_t run(const ProductArgs &a, hipStream_t stream) {
     if (a.K % kChunk == 0 && a.N % kChunk == 0)
-        return launch_product<DT, kRows, kCols, 128, 128, 2, 2, true, false>(a, stream);
-    return launch_product<DT, kRows, kCols, 128, 128, 2, 2, false, false>(a, stream);
+        return launch_tiles<DT, kRows, kCols, true, false>(a, stream);
+    return launch_tiles<DT, kRows, kCols, false, false>(a, stream);
 }
 
 }  // namespace

@@ -1,7 +1,10 @@
 // The gradient of a linear layer's weights, dw = dy^T x, from the INT8 payload of x
 // (include/fc/train.h, fc_linear_weight_grad): both operands are read down their
-// columns, and the codes become 16-bit values on their way into LDS. The kernel is
-// in fc_product.h.
+// columns. The codes become 16-bit values on their way into LDS, or, where many rows of
+// tiles would each do that again, in a launch of the dequantizer before the product.
+// Sums over many tokens for few outputs are split, and joined in a fixed order. The
+// kernel is in fc_product.h, the rules are in fc_product_dispatch.h.
+#include "fc_launch.h"
 #include "fc_product.h"
 
 namespace fc {
@@ -9,8 +12,9 @@ namespace {
 
 template <int DT>
 hipError_t run(const ProductArgs &a, hipStream_t stream) {
-    if (a.M % kChunk == 0) return launch_product<DT, kCols, kCodes, 128, 128, 2, 2, true, true>(a, stream);
-    return launch_product<DT, kCols, kCodes, 128, 128, 2, 2, false, true>(a, stream);
+    const bool direct = a.M % kChunk == 0;   // and columns are whole chunks: groups are
+    if (a.b != nullptr) return launch_tiles<DT, kCols, kCols, true, true>(a, stream);   // the plan's H % 8 == 0
+    return direct ? launch_tiles<DT, kCols, kCodes, true, true>(a, stream) : launch_tiles<DT, kCols, kCodes, false, true>(a, stream);
 }
 
 // dw (+)= the sum of the splits' parts, in their order
@@ -24,28 +28,36 @@ __global__ __launch_bounds__(kBlockThreads) void join_kernel(const float *part, 
 
 }  // namespace
 
-int weight_grad_splits(int R, int T, int K, int H) {
-    return 1;
-}
-
 hipError_t launch_linear_weight_grad(const uint16_t *dy, const Payload &px, int group, int dtype, int R,
-                                     int T, int K, int H, int accumulate, float *dw, float *part,
+                                     int T, int K, int H, int accumulate, float *dw, void *workspace,
                                      hipStream_t stream) {
+    const WeightGradPlan plan = weight_grad_plan(R, T, K, H);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    float *part = reinterpret_cast<float *>(ws + plan.value_bytes);
     ProductArgs p = {};
     p.a = dy;
-    p.pb = px;
-    p.group = group;
     p.R = R;
     p.M = H;
     p.N = K;
     p.K = T;
-    p.split = weight_grad_splits(R, T, K, H);
-    const int stages = (T - 1) / kStageK + 1;
-    p.split_k = (stages + p.split - 1) / p.split * kStageK;
-    p.split = (T - 1) / p.split_k + 1;   // no run is empty
+    p.group = group;
+    hipError_t err;
+    if (plan.value_bytes != 0) {
+        uint16_t *values = reinterpret_cast<uint16_t *>(ws);
+        const uint64_t n = (uint64_t)R * (uint64_t)T * (uint64_t)K;
+        const bool pow2 = (group & (group - 1)) == 0 && group <= 8192;
+        err = pow2 ? launch_dequantize(px.codes, px.s, px.z, n, 8, group, dtype, values, stream)
+                   : launch_dequantize_generic(px.codes, px.s, px.z, n, 8, group, dtype, nullptr, values, stream);
+        if (err != hipSuccess) return err;
+        p.b = values;
+    } else {
+        p.pb = px;
+    }
+    p.split = plan.split;
+    p.split_k = plan.split_k;
     p.out = p.split > 1 ? part : dw;
     p.accumulate = p.split > 1 ? 0 : accumulate;
-    hipError_t err = dtype == 0 ? run<0>(p, stream) : run<1>(p, stream);
+    err = dtype == 0 ? run<0>(p, stream) : run<1>(p, stream);
     if (err != hipSuccess || p.split == 1) return err;
     const uint64_t n = (uint64_t)R * (uint64_t)H * (uint64_t)K;
     hipLaunchKernelGGL(join_kernel, grid_of_blocks((n + kBlockThreads - 1) / kBlockThreads), dim3(kBlockThreads), 0, stream,

@@ -10,24 +10,25 @@
 // side by side (kCols: [k][m]; kCodes: [k][m] INT8 codes with scales and zeros).
 // Tiles of TM x TN outputs, stages of 64 k in LDS:
 //   - kRows: 64 k of a row are 128 bytes; its eight 16-byte chunks are rotated by
-//     (row / 2) % 8, so that the fragment reads (ds_read_b128: 32 rows x one chunk
-//     per half wave) meet each bank once;
+//     (row / 2) % 8, so that the fragment reads (ds_read_b128: 16 rows x one chunk
+//     per 16 lanes) meet each bank once;
 //   - kCols, kCodes: a stage is 64 rows of TM values; fragments are read with the
 //     transposing ds_read_b64_tr_b16 (16 lanes read 4 rows x 16 values and get 4 k
-//     of one column each). A half wave reads 64 bytes of 4 rows: their 64-byte
-//     units are swapped by k % 4, so that these meet each bank once as well.
+//     of one column each). A half wave reads 32 bytes of 8 rows: their 32-byte
+//     units are swapped by k % 4 and bit 3 of k, so that these meet each bank once.
 // 16-bit operands whose rows are whole 16-byte chunks go to LDS straight from
 // memory (buffer_load ... lds), the rotation done by which chunk a lane fetches;
 // others, and codes, go through registers: loads before a stage's products, stores
 // to LDS after them.
 //
-// v_mfma_f32_32x32x16: lane l holds row (column) l % 32 and k 8 (l / 32) + 0..7 of an
-// operand, and of the result column l % 32 and rows 8 (v / 4) + 4 (l / 32) + v % 4.
+// v_mfma_f32_16x16x32: lane l holds row (column) l % 16 and k 8 (l / 16) + 0..7 of an
+// operand, and of the result column l % 16 and rows 4 (l / 16) + 0..3.
 #pragma once
 
 #include "fc_act.h"
 #include "fc_grid.h"
 #include "fc_launch_train.h"
+#include "fc_product_dispatch.h"
 #include "fc_rows.h"
 
 namespace fc {
@@ -35,9 +36,10 @@ namespace {
 
 constexpr int kRows = 0, kCols = 1, kCodes = 2;
 constexpr int kStageK = 64;
+constexpr int kBlock = 16, kStepK = 32;         // of a matrix instruction
 constexpr int kChunk = 8;                      // values of a 16-byte chunk
 constexpr uint32_t kOutside = 0xFFFFFFF0u;     // an offset past every buffer
-constexpr int kRawBuffer = 0x00020000;         // resource word 3: raw 32-bit buffer
+constexpr uint32_t kRawBuffer = 0x00020000;         // resource word 3: raw 32-bit buffer
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -45,15 +47,16 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a8 __attribute__((aligned(8)));
 
 #define FC_LDS __attribute__((address_space(3)))
 
 template <int DT>
-__device__ __forceinline__ f32x16 mfma(const u32x4 &a, const u32x4 &b, const f32x16 &c) {
+__device__ __forceinline__ f32x4 mfma(const u32x4 &a, const u32x4 &b, const f32x4 &c) {
     if constexpr (DT == 1)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
 // Wait until at most N vector-memory operations of this wave are outstanding and
@@ -73,12 +76,26 @@ __device__ __forceinline__ void meet() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// 16 bytes per lane from offset base + off of a buffer (zeros past its end) to LDS at `to` + 16 * lane. The
+// instruction has no result register; whoever reads the LDS waits with wait_memory.
+// (The builtin for it would have the compiler wait for all such loads before every
+// transposing LDS read.) A write of M0 needs a wait state before its use, a resource
+// written by a vector instruction five.
+__device__ __forceinline__ void load_to_lds(const u32x4 &res, uint8_t FC_LDS *to, uint32_t off, uint32_t base) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"((uint32_t)(uintptr_t)to), "v"(off), "s"(res), "s"(base)
+                 : "memory", "m0");
+}
+
 struct ProductArgs {
     const uint16_t *a, *b;
     Payload pb;             // B of kCodes
     int group;
     int R, M, N, K;         // per rank
-    int tiles_m, tiles_n;
+    int from_m, from_n;     // the tiles cover rows [from_m, to_m) and columns [from_n, to_n)
+    int to_m, to_n;
+    int tiles_m, tiles_n;   // (these and total: set by the launcher)
     uint64_t total;         // tiles of all ranks and splits
     int split, split_k;     // k in `split` runs of split_k (a multiple of the stage)
     LinearEpilogue e;       // 16-bit results
@@ -98,19 +115,20 @@ template <int TM, int TN, int WM, int WN>
 struct Shape {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
     static constexpr int kSM = TM / WM, kSN = TN / WN;         // of a wave
-    static constexpr int kBM = kSM / 32, kBN = kSN / 32;
+    static constexpr int kBM = kSM / kBlock, kBN = kSN / kBlock;
     static constexpr int kBytesA = TM * kStageK * 2, kBytesB = TN * kStageK * 2, kStage = kBytesA + kBytesB;
     // the epilogue's rows of a wave: 32 rows of binary32, padded so that the two
     // halves of a wave (4 rows apart) write different banks
-    static constexpr int kPitch = kSN + 8;
+    static constexpr int kPitch = kSN + 4;
     static constexpr int kEpilogue = kWaves * 32 * kPitch * 4;
 };
 
-// Byte of the 64-byte-unit swap for row k of a kCols stage of W values.
+// Byte swap of 32-byte units for row k of a kCols stage of W values.
 template <int W>
 __device__ __forceinline__ uint32_t unit_swap(uint32_t k) {
-    if constexpr (W >= 128) return (k & 3u) << 6;
-    else return ((k >> 1) & 1u) << 6;
+    const uint32_t u = (k & 3u) | (k >> 1 & 4u);
+    if constexpr (W >= 128) return u << 5;
+    else return (u >> 1) << 5;
 }
 
 // Where 16-byte chunk `pos` of stage row `row` lies in LDS.
@@ -118,6 +136,14 @@ template <int OP, int W>
 __device__ __forceinline__ uint32_t chunk_at(uint32_t row, uint32_t pos) {
     if constexpr (OP == kRows) return row * (kStageK * 2) + ((pos ^ ((row >> 1) & 7u)) << 4);
     else return row * (W * 2) + ((pos << 4) ^ unit_swap<W>(row));
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, (int)kRawBuffer);
+}
+
+__device__ __forceinline__ uint32_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
 }
 
 // One operand's part of a workgroup: W rows (columns) in LDS at `lds`.
@@ -130,9 +156,12 @@ struct Stager {
     static_assert(kChunks % kThreads == 0, "whole chunks per thread");
     static constexpr int kLoads = DIRECT ? kPer : 0;                  // DMA loads in flight per stage
 
-    u32x4 raw[DIRECT || OP == kCodes ? 1 : kPer];
-    u32x2 code[OP == kCodes ? kPer : 1];
-    uint32_t sz[OP == kCodes ? kPer : 1];
+    // of codes a thread takes two neighbouring chunks at a time
+    static constexpr int kTurns = OP == kCodes ? kPer / 2 : kPer;
+    static_assert(OP != kCodes || kPer % 2 == 0, "pairs of chunks");
+
+    u32x4 raw[DIRECT ? 1 : kTurns];
+    uint32_t sz[OP == kCodes ? kTurns : 1][2];   // scale (low half) and zero of each chunk
 
     // Stage row and chunk of this thread's load j.
     static __device__ __forceinline__ void place(uint32_t tid, int j, uint32_t &row, uint32_t &pos) {
@@ -141,39 +170,41 @@ struct Stager {
         pos = c % kRowChunks;
     }
 
-    // p16: kRows the tile's first row, kCols the stage's first k row at the tile's
-    // first column; k_left: k from the stage's first to the end (positive).
-    __device__ __forceinline__ void direct(const uint16_t *p16, uint32_t ld, int live, int k_left, uint8_t FC_LDS *lds,
-                                           uint32_t tid) {
-        const uint32_t records = OP == kRows ? (uint32_t)live * ld * 2u : (uint32_t)(k_left < kStageK ? k_left : kStageK) * ld * 2u;
-        const __amdgpu_buffer_rsrc_t res =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p16), (short)0, (int)records, kRawBuffer);
+    // Byte offset of the thread's first chunk from the stage's first; turn j's lies
+    // kTurnRows memory rows further, at the same chunk and rotation.
+    static constexpr uint32_t kTurnRows = kThreads / kRowChunks;
+    static_assert(!DIRECT || kTurnRows % 16 == 0, "the rotations repeat from turn to turn");
+    static __device__ __forceinline__ uint32_t source(uint32_t tid) {
+        const uint32_t row = tid / kRowChunks, pos = tid % kRowChunks;
+        return OP == kRows ? pos ^ ((row >> 1) & 7u) : pos ^ (unit_swap<W>(row) >> 4);
+    }
+
+    // Turns [from, to) straight into LDS. p16: kRows the tile's first row at the stage's
+    // first k, kCols the stage's first k row at the tile's first column; k_left: k from
+    // the stage's first to the end (positive).
+    static __device__ __forceinline__ void direct(const uint16_t *p16, uint32_t ld, int live, int k_left, uint8_t FC_LDS *lds,
+                                                  uint32_t tid, int from, int to) {
+        const uint32_t records = (uint32_t)(OP == kRows ? live : k_left < kStageK ? k_left : kStageK) * ld * 2u;
+        const uint64_t at = reinterpret_cast<uint64_t>(p16);
+        const u32x4 res = {(uint32_t)at, (uint32_t)(at >> 32) & 0xFFFFu, records, kRawBuffer};
         const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const uint32_t src = source(tid);
+        uint32_t off = tid / kRowChunks * (ld * 2u) + src * 16u;
+        off = (int)(src * kChunk) < (OP == kRows ? k_left : live) ? off : kOutside;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            uint32_t row, pos, src;
-            place(tid, j, row, pos);
-            uint32_t off;
-            if constexpr (OP == kRows) {
-                src = pos ^ ((row >> 1) & 7u);
-                off = row * ld * 2u + src * 16u;
-                off = (int)(src * kChunk) < k_left ? off : kOutside;
-            } else {
-                src = pos ^ (unit_swap<W>(row) >> 4);
-                off = row * ld * 2u + src * 16u;
-                off = (int)(src * kChunk) < live ? off : kOutside;
-            }
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (FC_LDS void *)(lds + ((uint32_t)j * kThreads + wave * kWave) * 16u), 16,
-                                                     off, 0, 0, 0);
+            if (j < from || j >= to) continue;
+            load_to_lds(res, lds + ((uint32_t)j * kThreads + wave * kWave) * 16u, off, (uint32_t)j * kTurnRows * (ld * 2u));
         }
     }
 
-    // 16-bit values at any alignment and length, into registers.
-    __device__ __forceinline__ void fetch(const uint16_t *p16, uint32_t ld, int live, int k_left, uint32_t tid) {
+    // Turns [from, to): 16-bit values at any alignment and length, into registers.
+    __device__ __forceinline__ void fetch(const uint16_t *p16, uint32_t ld, int live, int k_left, uint32_t tid, int from, int to) {
         const int wide = OP == kRows ? k_left : live;       // values left along a memory row
         const int high = OP == kRows ? live : k_left;       // memory rows left
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
+        for (int j = 0; j < kTurns; ++j) {
+            if (j < from || j >= to) continue;
             uint32_t row, pos;
             place(tid, j, row, pos);
             const int e = (int)pos * kChunk;
@@ -194,62 +225,79 @@ struct Stager {
         }
     }
 
-    // Codes with their scale and zero: codes, s and z at the stage's first k row.
+    // Turns [from, to) of codes with their scales and zeros, always the same number of
+    // loads (3 a turn, 5 where chunks are not paired): what lies past the tile's columns or the rows reads as 0. A chunk
+    // that starts at the row's end belongs to columns that are not stored.
     __device__ __forceinline__ void fetch_codes(const uint8_t *codes, const uint16_t *s, const uint16_t *z, uint32_t ld,
-                                                uint32_t groups, uint32_t n0, uint32_t magic, int live, int k_left,
-                                                uint32_t tid) {
+                                                uint32_t groups, uint32_t n0, uint32_t magic, bool paired, int live, int k_left,
+                                                uint32_t tid, int from, int to) {
+        const uint32_t rows = (uint32_t)(k_left < kStageK ? k_left : kStageK);
+        const __amdgpu_buffer_rsrc_t cr = buffer_of(codes, rows * ld), sr = buffer_of(s, rows * groups * 2), zr = buffer_of(z, rows * groups * 2);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            uint32_t row, pos;
-            place(tid, j, row, pos);
-            const uint32_t e = pos * kChunk;
-            u32x2 v = {0, 0};
-            uint32_t m = 0;   // scale and zero 0: the value 0
-            if ((int)row < k_left && (int)e < live) {
-                v = *reinterpret_cast<const u32x2 *>(codes + (uint64_t)row * ld + n0 + e);
-                const uint64_t g = (uint64_t)row * groups + group_of((n0 + e) / kChunk, magic);
-                m = (uint32_t)s[g] | (uint32_t)z[g] << 16;
+        for (int j = 0; j < kTurns; ++j) {
+            if (j < from || j >= to) continue;
+            const uint32_t c = (tid + (uint32_t)j * kThreads) * 2;
+            const uint32_t row = c / kRowChunks, e = c % kRowChunks * kChunk;
+            const bool in = (int)e < live;
+            const uint32_t v = (n0 + e) / kChunk;
+            const uint32_t at = in ? row * ld + n0 + e : kOutside, g = in ? (row * groups + group_of(v, magic)) * 2 : kOutside;
+            raw[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(cr, (int)at, 0, 0));
+            sz[j][0] = load16(sr, g) | load16(zr, g) << 16;
+            sz[j][1] = sz[j][0];
+            if (!paired) {   // the two chunks may lie in two groups
+                const uint32_t h = in ? (row * groups + group_of(v + 1, magic)) * 2 : kOutside;
+                sz[j][1] = load16(sr, h) | load16(zr, h) << 16;
             }
-            code[j] = v;
-            sz[j] = m;
         }
     }
 
-    __device__ __forceinline__ void commit(uint8_t FC_LDS *lds, uint32_t tid) {
+    __device__ __forceinline__ void commit(uint8_t FC_LDS *lds, uint32_t tid, int from, int to) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            uint32_t row, pos;
-            place(tid, j, row, pos);
-            u32x4 v;
+        for (int j = 0; j < kTurns; ++j) {
+            if (j < from || j >= to) continue;
             if constexpr (OP == kCodes) {
-                const uint32_t w[2] = {code[j].x, code[j].y};
-                float x[kLaneElems];
-                dequant8<8>(w, (uint16_t)sz[j], (uint16_t)(sz[j] >> 16), x);
-                v = narrow8<DT>(x);
+                const uint32_t c = (tid + (uint32_t)j * kThreads) * 2;
+                const uint32_t row = c / kRowChunks, pos = c % kRowChunks;
+                const uint32_t w[2][2] = {{raw[j].x, raw[j].y}, {raw[j].z, raw[j].w}};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[kLaneElems];
+                    dequant8<8>(w[h], (uint16_t)sz[j][h], (uint16_t)(sz[j][h] >> 16), x);
+                    *(FC_LDS u32x4 *)(lds + chunk_at<OP, W>(row, pos + h)) = narrow8<DT>(x);
+                }
             } else {
-                v = raw[j];
+                uint32_t row, pos;
+                place(tid, j, row, pos);
+                *(FC_LDS u32x4 *)(lds + chunk_at<OP, W>(row, pos)) = raw[j];
             }
-            *(FC_LDS u32x4 *)(lds + chunk_at<OP, W>(row, pos)) = v;
         }
     }
 };
 
-// Fragment of 32 rows (columns) from `first` and 16 k from 16 ks.
+// Fragments of 16 rows (columns) and 32 k. at(): the lane's first byte in block 0 of
+// the wave, whose first row (column) is `first`; a block further and a step of k are
+// a constant added or XORed (the blocks' and steps' bits are free in it).
 template <int OP, int W>
-__device__ __forceinline__ u32x4 fragment(const uint8_t FC_LDS *lds, uint32_t first, uint32_t ks, uint32_t lane) {
-    if constexpr (OP == kRows) {
-        const uint32_t row = first + (lane & 31u);
-        return *(const FC_LDS u32x4 *)(lds + chunk_at<kRows, W>(row, 2 * ks + (lane >> 5)));
-    } else {
-        const uint32_t q = lane & 15u, k = ks * 16 + (lane >> 5) * 8 + (q >> 2);
-        const uint32_t col = (first + ((lane >> 4) & 1u) * 16 + (q & 3u) * 4) * 2;
-        const uint32_t at = k * (W * 2) + (col ^ unit_swap<W>(q >> 2));   // k % 4 is q / 4
-        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FC_LDS i16x4 *)(lds + at));
-        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FC_LDS i16x4 *)(lds + at + 4 * (W * 2)));
-        const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
-        return u32x4{l.x, l.y, h.x, h.y};
+struct Fragment {
+    static __device__ __forceinline__ uint32_t at(uint32_t first, uint32_t lane) {
+        const uint32_t q = lane & 15u, g = lane >> 4;
+        if constexpr (OP == kRows) return chunk_at<kRows, W>(first + q, g);
+        const uint32_t k = g * 8 + (q >> 2);
+        return k * (W * 2) + (((first + (q & 3u) * 4) * 2) ^ unit_swap<W>(k));   // k + 4 is swapped alike
     }
-}
+    static __device__ __forceinline__ u32x4 read(const uint8_t FC_LDS *lds, uint32_t at0, uint32_t block, uint32_t ks) {
+        if constexpr (OP == kRows) {
+            return *(const FC_LDS u32x4 *)(lds + (at0 ^ (ks << 6)) + block * (kBlock * kStageK * 2));
+        } else {
+            const uint32_t a = opaque(at0);   // the blocks' addresses are not kept from stage to stage
+            const uint8_t FC_LDS *p = lds + (a ^ (block << 5)) + ks * (kStepK * W * 2);
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FC_LDS i16x4 *)p);
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FC_LDS i16x4 *)(p + 4 * (W * 2)));
+            const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
+            return u32x4{l.x, l.y, h.x, h.y};
+        }
+    }
+};
 
 template <int DT>
 __device__ __forceinline__ void widen4(const uint16_t *p, int n, float (&v)[4]) {
@@ -316,11 +364,28 @@ __device__ __forceinline__ void finish4(const LinearEpilogue &e, uint64_t at, in
     store4<DT>(e.y + at, left, v);
 }
 
+// Workgroup b runs on XCD b % 8: each XCD takes its own run of the tiles, so that its
+// workgroups share operands in its L2.
+constexpr uint32_t kXcds = 8;
+__device__ __forceinline__ uint64_t by_xcd(uint64_t id, uint64_t total) {
+    const uint64_t q = total / kXcds, rest = total % kXcds;
+    const uint64_t x = id % kXcds;
+    return x * q + (x < rest ? x : rest) + id / kXcds;
+}
+
+// Tiles in groups of 4 rows, a group column by column.
+__device__ __forceinline__ void grouped(uint32_t tile, uint32_t tiles_m, uint32_t tiles_n, uint32_t &tm, uint32_t &tn) {
+    const uint32_t per = 4 * tiles_n, g = tile / per, in = tile - g * per;
+    const uint32_t rows = tiles_m - 4 * g < 4 ? tiles_m - 4 * g : 4;
+    tn = in / rows;
+    tm = 4 * g + in - tn * rows;
+}
+
 // F32: binary32 results (the weight gradient), else 16-bit ones with the epilogue.
 // DIRECT: 16-bit operands go to LDS straight from memory.
 template <int DT, int OPA, int OPB, int TM, int TN, int WM, int WN, bool DIRECT, bool F32>
-__global__ __launch_bounds__((Shape<TM, TN, WM, WN>::kThreads)) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void product_kernel(const ProductArgs a, uint32_t magic) {
+__global__ __launch_bounds__((Shape<TM, TN, WM, WN>::kThreads)) __attribute__((amdgpu_waves_per_eu(TM * TN < 128 * 128 ? 4 : 2)))
+void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
     using S = Shape<TM, TN, WM, WN>;
     constexpr int kLds = 2 * S::kStage > S::kEpilogue || F32 ? 2 * S::kStage : S::kEpilogue;
     __shared__ __attribute__((aligned(16))) uint8_t shared[kLds];
@@ -328,13 +393,16 @@ void product_kernel(const ProductArgs a, uint32_t magic) {
     const uint32_t tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63u;
     const int wave = (int)__builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const uint64_t id = grid_index();
-    if (id >= a.total) return;
+    const uint64_t flat = grid_index();
+    if (flat >= a.total) return;
+    const uint64_t id = by_xcd(flat, a.total);
     const uint64_t per = (uint64_t)a.tiles_m * (uint32_t)a.tiles_n;
     const uint64_t batch = id / per;                       // rank, then split
     const uint32_t tile = (uint32_t)(id - batch * per);
     const uint32_t r = (uint32_t)(batch % (uint32_t)a.R), part = (uint32_t)(batch / (uint32_t)a.R);
-    const int m0 = (int)(tile / (uint32_t)a.tiles_n) * TM, n0 = (int)(tile % (uint32_t)a.tiles_n) * TN;
+    uint32_t tm, tn;
+    grouped(tile, (uint32_t)a.tiles_m, (uint32_t)a.tiles_n, tm, tn);
+    const int m0 = a.from_m + (int)tm * TM, n0 = a.from_n + (int)tn * TN;
     const int64_t k0 = (int64_t)part * a.split_k;
     const int k_count = (int)(a.K - k0 < a.split_k ? a.K - k0 : a.split_k);
     const int stages = (k_count - 1) / kStageK + 1;
@@ -357,74 +425,119 @@ void product_kernel(const ProductArgs a, uint32_t magic) {
         pb = a.b + r * nk + (OPB == kRows ? (uint64_t)(uint32_t)n0 * ldb + k0 : k0 * ldb + (uint32_t)n0);
     }
 
+    constexpr bool kThroughRegs = !DIRECT || OPB == kCodes;   // some of a stage goes through registers
     Stager<DT, OPA, TM, S::kWaves, DIRECT> sa;
     Stager<DT, OPB, TN, S::kWaves, DIRECT && OPB != kCodes> sb;
-    // stage p: from memory into LDS buffer p % 2, or into registers
-    auto issue = [&](int p) {
-        const int64_t ko = (int64_t)p * kStageK;
-        const int left = k_count - p * kStageK;
-        const uint16_t *qa = pa + (OPA == kRows ? ko : ko * lda);
-        uint8_t FC_LDS *la = lds + (p & 1) * S::kStage, *lb = la + S::kBytesA;
-        if constexpr (DIRECT) sa.direct(qa, lda, live_m, left, la, tid);
-        else sa.fetch(qa, lda, live_m, left, tid);
-        if constexpr (OPB == kCodes) {
-            sb.fetch_codes(codes + ko * ldb, cs + ko * groups, cz + ko * groups, ldb, groups, (uint32_t)n0, magic, live_n, left, tid);
-        } else {
-            const uint16_t *qb = pb + (OPB == kRows ? ko : ko * ldb);
-            if constexpr (DIRECT) sb.direct(qb, ldb, live_n, left, lb, tid);
-            else sb.fetch(qb, ldb, live_n, left, tid);
+    // Part `part` of `parts` of stage p's loads straight into LDS buffer p % 2.
+    auto issue = [&](int p, int part, int parts) {
+        if constexpr (DIRECT) {
+            const int64_t ko = (int64_t)p * kStageK;
+            const int left = k_count - p * kStageK;
+            uint8_t FC_LDS *la = lds + (p & 1) * S::kStage, *lb = la + S::kBytesA;
+            constexpr int na = decltype(sa)::kPer, nb = decltype(sb)::kPer;
+            sa.direct(pa + (OPA == kRows ? ko : ko * lda), lda, live_m, left, la, tid, na * part / parts, na * (part + 1) / parts);
+            if constexpr (OPB != kCodes)
+                sb.direct(pb + (OPB == kRows ? ko : ko * ldb), ldb, live_n, left, lb, tid, nb * part / parts, nb * (part + 1) / parts);
         }
     };
-    auto commit = [&](int p) {
+    // The same for what goes through registers: into these, and from there to LDS.
+    auto fetch = [&](int p, int part, int parts) {
+        const int64_t ko = (int64_t)p * kStageK;
+        const int left = k_count - p * kStageK;
+        constexpr int na = decltype(sa)::kTurns, nb = decltype(sb)::kTurns;
+        if constexpr (!DIRECT)
+            sa.fetch(pa + (OPA == kRows ? ko : ko * lda), lda, live_m, left, tid, na * part / parts, na * (part + 1) / parts);
+        if constexpr (OPB == kCodes)
+            sb.fetch_codes(codes + ko * ldb, cs + ko * groups, cz + ko * groups, ldb, groups, (uint32_t)n0, magic, paired, live_n,
+                           left, tid, nb * part / parts, nb * (part + 1) / parts);
+        else if constexpr (!DIRECT)
+            sb.fetch(pb + (OPB == kRows ? ko : ko * ldb), ldb, live_n, left, tid, nb * part / parts, nb * (part + 1) / parts);
+    };
+    auto commit = [&](int p, int part, int parts) {
         uint8_t FC_LDS *la = lds + (p & 1) * S::kStage, *lb = la + S::kBytesA;
-        if constexpr (!DIRECT) sa.commit(la, tid);
-        if constexpr (!DIRECT || OPB == kCodes) sb.commit(lb, tid);
+        constexpr int na = decltype(sa)::kTurns, nb = decltype(sb)::kTurns;
+        if constexpr (!DIRECT) sa.commit(la, tid, na * part / parts, na * (part + 1) / parts);
+        if constexpr (kThroughRegs) sb.commit(lb, tid, nb * part / parts, nb * (part + 1) / parts);
     };
 
-    f32x16 acc[S::kBM][S::kBN];
+    f32x4 acc[S::kBM][S::kBN];
 #pragma unroll
     for (int i = 0; i < S::kBM; ++i)
 #pragma unroll
-        for (int j = 0; j < S::kBN; ++j) acc[i][j] = f32x16{};
+        for (int j = 0; j < S::kBN; ++j) acc[i][j] = f32x4{};
 
-    issue(0);
-    commit(0);
-    for (int p = 0; p < stages; ++p) {
-        // stage p is in LDS and every wave is done with stage p - 1, whose buffer
-        // stage p + 1 then fills
-        wait_memory<0>();
-        meet();
-        const bool more = p + 1 < stages;
-        if (more) issue(p + 1);
+    // A stage is 2 steps of 32 k. The fragments of a step are read during the products
+    // of the step before, those of a block of columns after that block's products. In the last step these are the next stage's: before it, each
+    // wave waits for its own loads of that stage (issued a stage ago) and the workgroup
+    // meets; from there on the buffer of this stage is free, every wave having read the
+    // last of it, and takes the loads of the stage after next. What goes through
+    // registers is written to LDS in the steps before the meeting, and its registers
+    // take the stage after next at once.
+    const uint32_t fa0 = Fragment<OPA, TM>::at((uint32_t)(wm * S::kSM), lane);
+    const uint32_t fb0 = Fragment<OPB, TN>::at((uint32_t)(wn * S::kSN), lane);
+    u32x4 fa[2][S::kBM], fb[S::kBN];
+    auto read = [&](int p, int ks, int part) {
         const uint8_t FC_LDS *la = lds + (p & 1) * S::kStage, *lb = la + S::kBytesA;
+        if (part < S::kBM) fa[ks & 1][part] = Fragment<OPA, TM>::read(la, fa0, (uint32_t)part, (uint32_t)ks);
+        fb[part] = Fragment<OPB, TN>::read(lb, fb0, (uint32_t)part, (uint32_t)ks);
+    };
+    static_assert(S::kBM <= S::kBN, "a part of a step has a block of columns");
+    auto step = [&](int ks, auto &&side) {
 #pragma unroll
-        for (uint32_t ks = 0; ks < kStageK / 16; ++ks) {
-            u32x4 fa[S::kBM], fb[S::kBN];
+        for (int j = 0; j < S::kBN; ++j) {
 #pragma unroll
-            for (int i = 0; i < S::kBM; ++i) fa[i] = fragment<OPA, TM>(la, (uint32_t)(wm * S::kSM + i * 32), ks, lane);
-#pragma unroll
-            for (int j = 0; j < S::kBN; ++j) fb[j] = fragment<OPB, TN>(lb, (uint32_t)(wn * S::kSN + j * 32), ks, lane);
-#pragma unroll
-            for (int i = 0; i < S::kBM; ++i)
-#pragma unroll
-                for (int j = 0; j < S::kBN; ++j) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j]);
+            for (int i = 0; i < S::kBM; ++i) acc[i][j] = mfma<DT>(fa[ks & 1][i], fb[j], acc[i][j]);
+            side(j);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (more) commit(p + 1);
+    };
+    constexpr int kSteps = kStageK / kStepK;
+    issue(0, 0, 1);
+    if constexpr (kThroughRegs) {
+        fetch(0, 0, 1);
+        commit(0, 0, 1);
+        if (stages > 1) fetch(1, 0, 1);
+    }
+    if (stages > 1) issue(1, 0, 1);
+    if (stages > 1 && !kThroughRegs) wait_memory<decltype(sa)::kLoads + decltype(sb)::kLoads>();
+    else wait_memory<0>();
+    meet();
+#pragma unroll
+    for (int j = 0; j < S::kBN; ++j) read(0, 0, j);
+    for (int p = 0; p < stages; ++p) {
+        const bool more = p + 1 < stages, after = p + 2 < stages;
+#pragma unroll
+        for (int ks = 0; ks < kSteps - 1; ++ks) {
+            if constexpr (kThroughRegs) {
+                if (more) commit(p + 1, ks, kSteps - 1);
+                if (after) fetch(p + 2, ks, kSteps - 1);
+            }
+            step(ks, [&](int j) { read(p, ks + 1, j); });
+        }
+        // the loads of the next stage into LDS are older than those into registers
+        if constexpr (!DIRECT) wait_memory<63>();
+        else if (!kThroughRegs || !after) wait_memory<0>();
+        else if (paired) wait_memory<3 * decltype(sb)::kTurns>();
+        else wait_memory<5 * decltype(sb)::kTurns>();
+        meet();
+        step(kSteps - 1, [&](int j) {
+            read(more ? p + 1 : p, 0, j);
+            if (after) issue(p + 2, j, S::kBN);
+        });
     }
 
     if constexpr (F32) {
-        // a row's 32 columns of a block are one line
         float *out = a.out + (uint64_t)batch * ((uint64_t)a.M * (uint32_t)a.N);
 #pragma unroll
         for (int i = 0; i < S::kBM; ++i)
 #pragma unroll
             for (int j = 0; j < S::kBN; ++j) {
-                const int n = n0 + wn * S::kSN + j * 32 + (int)(lane & 31u);
-                const int mb = m0 + wm * S::kSM + i * 32 + (int)(lane >> 5) * 4;
+                const int n = n0 + wn * S::kSN + j * kBlock + (int)(lane & 15u);
+                const int mb = m0 + wm * S::kSM + i * kBlock + (int)(lane >> 4) * 4;
                 if (n < a.N) {
 #pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        const int m = mb + 8 * (v / 4) + v % 4;
+                    for (int v = 0; v < 4; ++v) {
+                        const int m = mb + v;
                         if (m < a.M) {
                             float *o = out + (uint64_t)(uint32_t)m * (uint32_t)a.N + (uint32_t)n;
                             *o = a.accumulate ? *o + acc[i][j][v] : acc[i][j][v];
@@ -442,15 +555,17 @@ void product_kernel(const ProductArgs a, uint32_t magic) {
         float bias[4] = {};
         if (a.e.bias != nullptr && left > 0) widen4<DT>(a.e.bias + (uint64_t)r * (uint32_t)a.N + (uint32_t)n, left, bias);
 #pragma unroll
-        for (int i = 0; i < S::kBM; ++i) {
+        for (int i = 0; i < S::kBM; i += 2) {
 #pragma unroll
-            for (int j = 0; j < S::kBN; ++j)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int v = 0; v < 16; ++v)
-                    mine[(8 * (v / 4) + 4 * (lane >> 5) + v % 4) * S::kPitch + j * 32 + (lane & 31u)] = acc[i][j][v];
+                for (int j = 0; j < S::kBN; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        mine[(h * kBlock + 4 * (lane >> 4) + v) * S::kPitch + j * kBlock + (lane & 15u)] = acc[i + h][j][v];
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             for (int t = 0; t < 32; t += kRowsTurn) {
-                const int row = t + (int)(lane / kLanesRow), m = m0 + wm * S::kSM + i * 32 + row;
+                const int row = t + (int)(lane / kLanesRow), m = m0 + wm * S::kSM + i * kBlock + row;
                 const f32x4 w = *(const FC_LDS f32x4 *)(mine + row * S::kPitch + c);
                 float v[4] = {w.x, w.y, w.z, w.w};
                 if (m < a.M && left > 0)
@@ -464,8 +579,8 @@ void product_kernel(const ProductArgs a, uint32_t magic) {
 template <int DT, int OPA, int OPB, int TM, int TN, int WM, int WN, bool DIRECT, bool F32>
 hipError_t launch_product(ProductArgs a, hipStream_t stream) {
     using S = Shape<TM, TN, WM, WN>;
-    a.tiles_m = (a.M - 1) / TM + 1;
-    a.tiles_n = (a.N - 1) / TN + 1;
+    a.tiles_m = (a.to_m - a.from_m - 1) / TM + 1;
+    a.tiles_n = (a.to_n - a.from_n - 1) / TN + 1;
     a.total = (uint64_t)a.tiles_m * (uint64_t)a.tiles_n * (uint64_t)a.R * (uint64_t)a.split;
     uint32_t magic = 0;
     if (OPB == kCodes && a.group != kChunk) {
@@ -473,8 +588,36 @@ hipError_t launch_product(ProductArgs a, hipStream_t stream) {
         magic = (uint32_t)(((uint64_t(1) << 32) + d - 1) / d);
     }
     hipLaunchKernelGGL((product_kernel<DT, OPA, OPB, TM, TN, WM, WN, DIRECT, F32>), grid_of_blocks(a.total),
-                       dim3(S::kThreads), 0, stream, a, magic);
+                       dim3(S::kThreads), 0, stream, a, magic, a.group % (2 * kChunk) == 0);
     return hipGetLastError();
+}
+
+// A product's tiles: those of 256 over the region that fills the device with them in
+// whole rounds, smaller ones over the rest (fc_product_dispatch.h).
+template <int DT, int OPA, int OPB, bool DIRECT, bool F32>
+hipError_t launch_tiles(ProductArgs a, hipStream_t stream) {
+    const int cus = compute_units();
+    if (cus <= 0) return hipErrorInvalidDevice;
+    constexpr bool kLarge = DIRECT && OPB != kCodes;
+    const ProductPlan plan = product_plan(a.R * a.split, a.M, a.N, cus, kLarge);
+    for (const ProductPlan::Part &p : plan.part) {
+        if (p.tile == 0) continue;
+        a.from_m = p.from_m;
+        a.from_n = p.from_n;
+        a.to_m = p.to_m;
+        a.to_n = p.to_n;
+        hipError_t err;
+        if (p.tile == 64) {
+            err = launch_product<DT, OPA, OPB, 64, 64, 2, 2, DIRECT, F32>(a, stream);
+        } else if (p.tile == 128) {
+            err = launch_product<DT, OPA, OPB, 128, 128, 2, 2, DIRECT, F32>(a, stream);
+        } else {
+            if constexpr (kLarge) err = launch_product<DT, OPA, OPB, 256, 256, 4, 2, DIRECT, F32>(a, stream);
+            else err = hipErrorInvalidValue;
+        }
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace

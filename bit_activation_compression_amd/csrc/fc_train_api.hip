@@ -6,6 +6,7 @@
 #include "fc_grid.h"
 #include "fc_launch.h"
 #include "fc_launch_train.h"
+#include "fc_product_dispatch.h"
 #include "fc_validate_train.h"
 
 namespace fc {
@@ -285,8 +286,8 @@ fc_status fc_linear_input_grad(const void *dy, const void *w, fc_dtype dt, int R
 
 size_t fc_linear_weight_grad_workspace_bytes(int R, int T, int K, int H) {
     if (check_product(R, T, K, H) != FC_OK || T == 0 || K > FC_TRAIN_MAX_ROW) return 0;
-    const int split = fc::weight_grad_splits(R, T, K, H);
-    return split > 1 ? (size_t)split * elems(R, H, K) * 4 : 0;
+    const fc::WeightGradPlan plan = fc::weight_grad_plan(R, T, K, H);
+    return plan.value_bytes + plan.part_bytes;
 }
 
 fc_status fc_linear_weight_grad(const void *dy, const uint8_t *codes, const uint16_t *s,
@@ -313,7 +314,7 @@ fc_status fc_linear_weight_grad(const void *dy, const uint8_t *codes, const uint
     st = check_overlap({ws, wk}, {ds, cs, ss, zs});
     if (st != FC_OK) return st;
     return from_hip(fc::launch_linear_weight_grad(u16(dy), {codes, s, z}, group, (int)dt, R, T, K, H, accumulate, dw,
-                                                  f32(workspace), stream_of(stream)));
+                                                  workspace, stream_of(stream)));
 }
 
 }  // extern "C"
