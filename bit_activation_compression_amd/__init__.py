@@ -32,7 +32,8 @@ __all__ = [
     "fc_linear_mxfp4_workspace_bytes", "LAYER_SYMBOLS",
     "fc_layer_norm", "fc_layer_norm_backward", "fc_linear_act", "fc_linear_input_grad",
     "fc_linear_weight_grad", "fc_activation_backward", "fc_layer_norm_backward_workspace_bytes",
-    "fc_linear_weight_grad_workspace_bytes", "fc_activation_backward_workspace_bytes", "ACTIVATIONS",
+    "fc_linear_weight_grad_workspace_bytes", "fc_activation_backward_workspace_bytes",
+    "fc_linear_act_workspace_bytes", "fc_linear_input_grad_workspace_bytes", "ACTIVATIONS",
     "TRAIN_SYMBOLS",
 ]
 
@@ -59,6 +60,7 @@ TRAIN_SYMBOLS = (
     "fc_layer_norm", "fc_layer_norm_backward", "fc_linear_act", "fc_linear_input_grad",
     "fc_linear_weight_grad", "fc_activation_backward", "fc_layer_norm_backward_workspace_bytes",
     "fc_linear_weight_grad_workspace_bytes", "fc_activation_backward_workspace_bytes",
+    "fc_linear_act_workspace_bytes", "fc_linear_input_grad_workspace_bytes",
 )
 ACTIVATIONS = ("none", "relu", "silu", "gelu", "gelu_tanh")   # their places are the C ABI's fc_act
 # FC_NOALLOC_SCRATCH_BYTES of include/fc.h: the payload scratch the library holds per device
@@ -119,18 +121,20 @@ def lib() -> ctypes.CDLL:
             L.fc_linear_mxfp4_workspace_bytes.restype = Z
             L.fc_layer_norm.argtypes = [P, I, I, I, P, P, F, I, P, P, P, P, P, P, I, P]
             L.fc_layer_norm_backward.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P, P, P, P, P, P, Z, P]
-            L.fc_linear_act.argtypes = [P, P, I, I, I, I, I, P, I, P, P, P, P, P]
-            L.fc_linear_input_grad.argtypes = [P, P, I, I, I, I, I, P, P, P]
+            L.fc_linear_act.argtypes = [P, P, I, I, I, I, I, P, I, P, P, P, P, P, Z, P]
+            L.fc_linear_input_grad.argtypes = [P, P, I, I, I, I, I, P, P, P, Z, P]
             L.fc_linear_weight_grad.argtypes = [P, P, P, P, I, I, I, I, I, I, I, P, P, Z, P]
             L.fc_activation_backward.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, P, Z, P]
             for f in (L.fc_layer_norm, L.fc_layer_norm_backward, L.fc_linear_act, L.fc_linear_input_grad,
                       L.fc_linear_weight_grad, L.fc_activation_backward):
                 f.restype = I
             L.fc_layer_norm_backward_workspace_bytes.argtypes = [I, I]
-            L.fc_linear_weight_grad_workspace_bytes.argtypes = [I, I, I, I]
+            for f in (L.fc_linear_weight_grad_workspace_bytes, L.fc_linear_act_workspace_bytes,
+                      L.fc_linear_input_grad_workspace_bytes):
+                f.argtypes = [I, I, I, I]
+                f.restype = Z
             L.fc_activation_backward_workspace_bytes.argtypes = [I, I, I]
-            for f in (L.fc_layer_norm_backward_workspace_bytes, L.fc_linear_weight_grad_workspace_bytes,
-                      L.fc_activation_backward_workspace_bytes):
+            for f in (L.fc_layer_norm_backward_workspace_bytes, L.fc_activation_backward_workspace_bytes):
                 f.restype = Z
             L.fc_workspace_bytes_mixed.argtypes = [I, I, I, I, I, I]
             L.fc_workspace_bytes_mixed.restype = Z
@@ -839,8 +843,13 @@ def _product(x: torch.Tensor, w: torch.Tensor, name: str):
     return R, T, n, H, K
 
 
+def fc_linear_act_workspace_bytes(R: int, T: int, K: int, H: int) -> int:
+    _ints(R=R, T=T, K=K, H=H)
+    return (_lib or lib()).fc_linear_act_workspace_bytes(R, T, K, H)
+
+
 def fc_linear_act(a: torch.Tensor, w: torch.Tensor, bias=None, act: str = "none", mul=None, residual=None,
-                  y=None, z=None, stream=None):
+                  y=None, z=None, workspace=None, stream=None):
     """a [R, T, K] times w [R, H, K] (or both without R; fp16/bf16) -> (y, z):
         z = a w^T + bias,  y = act(z) * mul + residual
     with bias [R, H], mul and residual [R, T, H]. z is rounded and returned where a tensor (or
@@ -861,11 +870,18 @@ def fc_linear_act(a: torch.Tensor, w: torch.Tensor, bias=None, act: str = "none"
         z = None
     elif z is not None:
         z, pz = _out(None if z is True else z, "z", a, rows, dt, stream)
-    _launch("fc_linear_act", dev, stream, pa, pw, code, R, T, K, H, pb, _act(act), pm, pr, py, pz)
+    need = (_lib or lib()).fc_linear_act_workspace_bytes(R, T, K, H)
+    workspace, pk, have = _room_for(workspace, need, a, stream)
+    _launch("fc_linear_act", dev, stream, pa, pw, code, R, T, K, H, pb, _act(act), pm, pr, py, pz, pk, have)
     return y, z
 
 
-def fc_linear_input_grad(dy: torch.Tensor, w: torch.Tensor, residual=None, dx=None, stream=None):
+def fc_linear_input_grad_workspace_bytes(R: int, T: int, K: int, H: int) -> int:
+    _ints(R=R, T=T, K=K, H=H)
+    return (_lib or lib()).fc_linear_input_grad_workspace_bytes(R, T, K, H)
+
+
+def fc_linear_input_grad(dy: torch.Tensor, w: torch.Tensor, residual=None, dx=None, workspace=None, stream=None):
     """dy [R, T, H] times w [R, H, K] (or both without R) -> dx [R, T, K] = dy w + residual, the
     gradient of the layer's input. residual [R, T, K] (None: 0) may be `dx` itself."""
     R, T, H, Hw, K = _product(dy, w, "dy")
@@ -877,7 +893,9 @@ def fc_linear_input_grad(dy: torch.Tensor, w: torch.Tensor, residual=None, dx=No
     pd, pw = _like(dy, "dy", tuple(dy.shape), dt, dev), _like(w, "w", tuple(w.shape), dt, dev)
     pr = _optional(residual, "residual", rows, dt, dev)
     dx, px = _out(dx, "dx", dy, rows, dt, stream)
-    _launch("fc_linear_input_grad", dev, stream, pd, pw, code, R, T, K, H, pr, px)
+    need = (_lib or lib()).fc_linear_input_grad_workspace_bytes(R, T, K, H)
+    workspace, pk, have = _room_for(workspace, need, dy, stream)
+    _launch("fc_linear_input_grad", dev, stream, pd, pw, code, R, T, K, H, pr, px, pk, have)
     return dx
 
 

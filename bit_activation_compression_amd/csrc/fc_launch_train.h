@@ -83,12 +83,14 @@ struct LinearEpilogue {
     uint16_t *y, *z;
     int act;
 };
-// a [R][T][K], w [R][H][K], bias [R][H], the others [R][T][H]
+// a [R][T][K], w [R][H][K], bias [R][H], the others [R][T][H]; workspaces as
+// linear_plan (fc_product_dispatch.h) has them
 hipError_t launch_linear_act(const uint16_t *a, const uint16_t *w, int dtype, int R, int T, int K, int H,
-                             const LinearEpilogue &e, hipStream_t stream);
+                             const LinearEpilogue &e, void *workspace, hipStream_t stream);
 // dx[r] = dy[r] w[r] (+ residual): dy [R][T][H], w [R][H][K], dx and residual [R][T][K]
 hipError_t launch_linear_input_grad(const uint16_t *dy, const uint16_t *w, int dtype, int R, int T, int K,
-                                    int H, const uint16_t *residual, uint16_t *dx, hipStream_t stream);
+                                    int H, const uint16_t *residual, uint16_t *dx, void *workspace,
+                                    hipStream_t stream);
 // dw[r] (+)= dy[r]^T x[r] for x a payload [R][T][K]; workspace as weight_grad_plan
 // (fc_product_dispatch.h) has it
 hipError_t launch_linear_weight_grad(const uint16_t *dy, const Payload &px, int group, int dtype, int R,

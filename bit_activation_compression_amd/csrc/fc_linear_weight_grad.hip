@@ -53,8 +53,8 @@ hipError_t launch_linear_weight_grad(const uint16_t *dy, const Payload &px, int 
     } else {
         p.pb = px;
     }
-    p.split = plan.split;
-    p.split_k = plan.split_k;
+    p.split = plan.split.split;
+    p.split_k = plan.split.split_k;
     p.out = p.split > 1 ? part : dw;
     p.accumulate = p.split > 1 ? 0 : accumulate;
     err = dtype == 0 ? run<0>(p, stream) : run<1>(p, stream);

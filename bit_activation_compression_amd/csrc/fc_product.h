@@ -111,12 +111,15 @@ struct Operand {
     int live;               // rows (kRows) or columns (kCols) that exist, from m0
 };
 
-template <int TM, int TN, int WM, int WN>
+template <int TM, int TN, int WM, int WN, int NS>
 struct Shape {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
     static constexpr int kSM = TM / WM, kSN = TN / WN;         // of a wave
     static constexpr int kBM = kSM / kBlock, kBN = kSN / kBlock;
     static constexpr int kBytesA = TM * kStageK * 2, kBytesB = TN * kStageK * 2, kStage = kBytesA + kBytesB;
+    static constexpr int kRing = NS * kStage;                  // stages in LDS
+    // waves that share a SIMD: of the workgroups that fit the LDS, but at most 4
+    static constexpr int kGroups = 160 * 1024 / kRing, kPerSimd = kGroups * kWaves / 4 < 4 ? kGroups * kWaves / 4 : 4;
     // the epilogue's rows of a wave: 32 rows of binary32, padded so that the two
     // halves of a wave (4 rows apart) write different banks
     static constexpr int kPitch = kSN + 4;
@@ -383,11 +386,11 @@ __device__ __forceinline__ void grouped(uint32_t tile, uint32_t tiles_m, uint32_
 
 // F32: binary32 results (the weight gradient), else 16-bit ones with the epilogue.
 // DIRECT: 16-bit operands go to LDS straight from memory.
-template <int DT, int OPA, int OPB, int TM, int TN, int WM, int WN, bool DIRECT, bool F32>
-__global__ __launch_bounds__((Shape<TM, TN, WM, WN>::kThreads)) __attribute__((amdgpu_waves_per_eu(TM * TN < 128 * 128 ? 4 : 2)))
+template <int DT, int OPA, int OPB, int TM, int TN, int WM, int WN, int NS, bool DIRECT, bool F32>
+__global__ __launch_bounds__((Shape<TM, TN, WM, WN, NS>::kThreads)) __attribute__((amdgpu_waves_per_eu(Shape<TM, TN, WM, WN, NS>::kPerSimd)))
 void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
-    using S = Shape<TM, TN, WM, WN>;
-    constexpr int kLds = 2 * S::kStage > S::kEpilogue || F32 ? 2 * S::kStage : S::kEpilogue;
+    using S = Shape<TM, TN, WM, WN, NS>;
+    constexpr int kLds = S::kRing > S::kEpilogue || F32 ? S::kRing : S::kEpilogue;
     __shared__ __attribute__((aligned(16))) uint8_t shared[kLds];
     uint8_t FC_LDS *lds = (uint8_t FC_LDS *)shared;
     const uint32_t tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63u;
@@ -428,12 +431,12 @@ void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
     constexpr bool kThroughRegs = !DIRECT || OPB == kCodes;   // some of a stage goes through registers
     Stager<DT, OPA, TM, S::kWaves, DIRECT> sa;
     Stager<DT, OPB, TN, S::kWaves, DIRECT && OPB != kCodes> sb;
-    // Part `part` of `parts` of stage p's loads straight into LDS buffer p % 2.
-    auto issue = [&](int p, int part, int parts) {
+    // Part `part` of `parts` of stage p's loads straight into the ring's place `at`.
+    auto issue = [&](int p, uint32_t at, int part, int parts) {
         if constexpr (DIRECT) {
             const int64_t ko = (int64_t)p * kStageK;
             const int left = k_count - p * kStageK;
-            uint8_t FC_LDS *la = lds + (p & 1) * S::kStage, *lb = la + S::kBytesA;
+            uint8_t FC_LDS *la = lds + at, *lb = la + S::kBytesA;
             constexpr int na = decltype(sa)::kPer, nb = decltype(sb)::kPer;
             sa.direct(pa + (OPA == kRows ? ko : ko * lda), lda, live_m, left, la, tid, na * part / parts, na * (part + 1) / parts);
             if constexpr (OPB != kCodes)
@@ -453,8 +456,8 @@ void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
         else if constexpr (!DIRECT)
             sb.fetch(pb + (OPB == kRows ? ko : ko * ldb), ldb, live_n, left, tid, nb * part / parts, nb * (part + 1) / parts);
     };
-    auto commit = [&](int p, int part, int parts) {
-        uint8_t FC_LDS *la = lds + (p & 1) * S::kStage, *lb = la + S::kBytesA;
+    auto commit = [&](uint32_t at, int part, int parts) {
+        uint8_t FC_LDS *la = lds + at, *lb = la + S::kBytesA;
         constexpr int na = decltype(sa)::kTurns, nb = decltype(sb)::kTurns;
         if constexpr (!DIRECT) sa.commit(la, tid, na * part / parts, na * (part + 1) / parts);
         if constexpr (kThroughRegs) sb.commit(lb, tid, nb * part / parts, nb * (part + 1) / parts);
@@ -467,19 +470,20 @@ void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
         for (int j = 0; j < S::kBN; ++j) acc[i][j] = f32x4{};
 
     // A stage is 2 steps of 32 k. The fragments of a step are read during the products
-    // of the step before, those of a block of columns after that block's products. In the last step these are the next stage's: before it, each
-    // wave waits for its own loads of that stage (issued a stage ago) and the workgroup
-    // meets; from there on the buffer of this stage is free, every wave having read the
-    // last of it, and takes the loads of the stage after next. What goes through
-    // registers is written to LDS in the steps before the meeting, and its registers
-    // take the stage after next at once.
+    // of the step before, those of a block of columns after that block's products. In
+    // the last step these are the next stage's: after its first products each wave waits
+    // for its own loads of that stage and the workgroup meets; from there on the place
+    // of this stage is free, every wave having read the last of it, and takes the loads
+    // of the stage NS further. What goes through registers is written to LDS in the step
+    // before the meeting, and its registers take the stage after next at once.
     const uint32_t fa0 = Fragment<OPA, TM>::at((uint32_t)(wm * S::kSM), lane);
     const uint32_t fb0 = Fragment<OPB, TN>::at((uint32_t)(wn * S::kSN), lane);
     u32x4 fa[2][S::kBM], fb[S::kBN];
-    auto read = [&](int p, int ks, int part) {
-        const uint8_t FC_LDS *la = lds + (p & 1) * S::kStage, *lb = la + S::kBytesA;
-        if (part < S::kBM) fa[ks & 1][part] = Fragment<OPA, TM>::read(la, fa0, (uint32_t)part, (uint32_t)ks);
-        fb[part] = Fragment<OPB, TN>::read(lb, fb0, (uint32_t)part, (uint32_t)ks);
+    auto read_a = [&](uint32_t at, int ks, int i) {
+        if (i >= 0 && i < S::kBM) fa[ks & 1][i] = Fragment<OPA, TM>::read(lds + at, fa0, (uint32_t)i, (uint32_t)ks);
+    };
+    auto read_b = [&](uint32_t at, int ks, int j) {
+        fb[j] = Fragment<OPB, TN>::read(lds + at + S::kBytesA, fb0, (uint32_t)j, (uint32_t)ks);
     };
     static_assert(S::kBM <= S::kBN, "a part of a step has a block of columns");
     auto step = [&](int ks, auto &&side) {
@@ -492,38 +496,68 @@ void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
         }
     };
     constexpr int kSteps = kStageK / kStepK;
-    issue(0, 0, 1);
+    // products of the last step before the meeting: they cover the last reads' latency
+    constexpr int kBefore = 1;
+    static_assert(S::kBN - kBefore + 1 >= S::kBM, "the next stage's rows are read after the meeting");
+    constexpr int kLoads = decltype(sa)::kLoads + decltype(sb)::kLoads;   // straight into LDS, a wave's of a stage
+    static_assert(NS == 2 || !kThroughRegs, "what goes through registers is one stage ahead");
     if constexpr (kThroughRegs) {
         fetch(0, 0, 1);
         commit(0, 0, 1);
         if (stages > 1) fetch(1, 0, 1);
     }
-    if (stages > 1) issue(1, 0, 1);
-    if (stages > 1 && !kThroughRegs) wait_memory<decltype(sa)::kLoads + decltype(sb)::kLoads>();
+#pragma unroll
+    for (int p = 0; p < NS; ++p)
+        if (p < stages) issue(p, (uint32_t)p * S::kStage, 0, 1);
+    if (!kThroughRegs && stages >= NS) wait_memory<(NS - 1) * kLoads>();
     else wait_memory<0>();
     meet();
 #pragma unroll
-    for (int j = 0; j < S::kBN; ++j) read(0, 0, j);
+    for (int j = 0; j < S::kBN; ++j) {
+        read_a(0, 0, j);
+        read_b(0, 0, j);
+    }
+    uint32_t here = 0;   // the ring's place of stage p
     for (int p = 0; p < stages; ++p) {
-        const bool more = p + 1 < stages, after = p + 2 < stages;
+        const uint32_t next = here + S::kStage == S::kRing ? 0 : here + S::kStage;
+        const bool more = p + 1 < stages, after = p + 2 < stages, ahead = p + NS < stages;
 #pragma unroll
         for (int ks = 0; ks < kSteps - 1; ++ks) {
             if constexpr (kThroughRegs) {
-                if (more) commit(p + 1, ks, kSteps - 1);
+                if (more) commit(next, ks, kSteps - 1);
                 if (after) fetch(p + 2, ks, kSteps - 1);
             }
-            step(ks, [&](int j) { read(p, ks + 1, j); });
+            step(ks, [&](int j) {
+                read_a(here, ks + 1, j);
+                read_b(here, ks + 1, j);
+            });
         }
-        // the loads of the next stage into LDS are older than those into registers
-        if constexpr (!DIRECT) wait_memory<63>();
-        else if (!kThroughRegs || !after) wait_memory<0>();
-        else if (paired) wait_memory<3 * decltype(sb)::kTurns>();
-        else wait_memory<5 * decltype(sb)::kTurns>();
-        meet();
         step(kSteps - 1, [&](int j) {
-            read(more ? p + 1 : p, 0, j);
-            if (after) issue(p + 2, j, S::kBN);
+            if (j < kBefore - 1) return;
+            const uint32_t from = more ? next : here;
+            if (j == kBefore - 1) {
+                // Stage p + 1 has landed: the loads of the later ones, and what was fetched
+                // into registers meanwhile, are younger.
+                if constexpr (!DIRECT) {
+                    wait_memory<63>();
+                } else if constexpr (kThroughRegs) {
+                    if (!after) wait_memory<0>();
+                    else if (paired) wait_memory<3 * decltype(sb)::kTurns>();
+                    else wait_memory<5 * decltype(sb)::kTurns>();
+                } else {
+                    if (p + NS - 1 < stages) wait_memory<(NS - 2) * kLoads>();
+                    else wait_memory<0>();
+                }
+                meet();
+#pragma unroll
+                for (int i = 0; i < kBefore; ++i) read_b(from, 0, i);
+            } else {
+                read_b(from, 0, j);
+            }
+            read_a(from, 0, j - kBefore + 1);
+            if (ahead) issue(p + NS, here, j - kBefore + 1, S::kBN - kBefore + 1);
         });
+        here = next;
     }
 
     if constexpr (F32) {
@@ -576,9 +610,9 @@ void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
     }
 }
 
-template <int DT, int OPA, int OPB, int TM, int TN, int WM, int WN, bool DIRECT, bool F32>
+template <int DT, int OPA, int OPB, int TM, int TN, int WM, int WN, int NS, bool DIRECT, bool F32>
 hipError_t launch_product(ProductArgs a, hipStream_t stream) {
-    using S = Shape<TM, TN, WM, WN>;
+    using S = Shape<TM, TN, WM, WN, NS>;
     a.tiles_m = (a.to_m - a.from_m - 1) / TM + 1;
     a.tiles_n = (a.to_n - a.from_n - 1) / TN + 1;
     a.total = (uint64_t)a.tiles_m * (uint64_t)a.tiles_n * (uint64_t)a.R * (uint64_t)a.split;
@@ -587,7 +621,7 @@ hipError_t launch_product(ProductArgs a, hipStream_t stream) {
         const uint64_t d = (uint64_t)(a.group / kChunk);
         magic = (uint32_t)(((uint64_t(1) << 32) + d - 1) / d);
     }
-    hipLaunchKernelGGL((product_kernel<DT, OPA, OPB, TM, TN, WM, WN, DIRECT, F32>), grid_of_blocks(a.total),
+    hipLaunchKernelGGL((product_kernel<DT, OPA, OPB, TM, TN, WM, WN, NS, DIRECT, F32>), grid_of_blocks(a.total),
                        dim3(S::kThreads), 0, stream, a, magic, a.group % (2 * kChunk) == 0);
     return hipGetLastError();
 }
@@ -607,17 +641,57 @@ hipError_t launch_tiles(ProductArgs a, hipStream_t stream) {
         a.to_m = p.to_m;
         a.to_n = p.to_n;
         hipError_t err;
-        if (p.tile == 64) {
-            err = launch_product<DT, OPA, OPB, 64, 64, 2, 2, DIRECT, F32>(a, stream);
-        } else if (p.tile == 128) {
-            err = launch_product<DT, OPA, OPB, 128, 128, 2, 2, DIRECT, F32>(a, stream);
+        if (p.tile == kSmallTile) {
+            err = launch_product<DT, OPA, OPB, 64, 64, 2, 2, kLarge ? 4 : 2, DIRECT, F32>(a, stream);
+        } else if (p.tile == kMiddleTile) {
+            err = launch_product<DT, OPA, OPB, 128, 128, 2, 2, 2, DIRECT, F32>(a, stream);
         } else {
-            if constexpr (kLarge) err = launch_product<DT, OPA, OPB, 256, 256, 4, 2, DIRECT, F32>(a, stream);
+            if constexpr (kLarge) err = launch_product<DT, OPA, OPB, 256, 256, 4, 2, 2, DIRECT, F32>(a, stream);
             else err = hipErrorInvalidValue;
         }
         if (err != hipSuccess) return err;
     }
     return hipSuccess;
+}
+
+// The epilogue of a product whose sums are split: binary32 parts [split][n] of
+// [R][M][N], added in their order, 4 columns of a row to a thread.
+template <int DT>
+__global__ __launch_bounds__(kBlockThreads) void join_epilogue_kernel(const float *part, int split, uint64_t rows, int M, int N,
+                                                                      LinearEpilogue e) {
+    const uint32_t quads = ((uint32_t)N + 3) / 4;
+    const uint64_t i = grid_index() * kBlockThreads + __builtin_amdgcn_workitem_id_x();
+    const uint64_t row = i / quads;
+    if (row >= rows) return;
+    const int n = (int)(i - row * quads) * 4, left = N - n;
+    const uint64_t at = row * (uint32_t)N + (uint32_t)n, all = rows * (uint32_t)N;
+    float v[4] = {};
+    for (int p = 0; p < split; ++p) {
+        const float *q = part + (uint64_t)p * all + at;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] += k < left ? q[k] : 0.0f;
+    }
+    float bias[4] = {};
+    if (e.bias != nullptr) widen4<DT>(e.bias + row / (uint32_t)M * (uint32_t)N + (uint32_t)n, left, bias);
+    finish4<DT>(e, at, left, bias, v);
+}
+
+// A product with the linear layer's epilogue, its sums split as `plan` has it (few
+// outputs: tiles of 64).
+template <int DT, int OPA, int OPB, bool DIRECT>
+hipError_t launch_split(ProductArgs a, const SplitPlan &plan, float *part, hipStream_t stream) {
+    a.split = plan.split;
+    a.split_k = plan.split_k;
+    if (plan.split == 1) return launch_tiles<DT, OPA, OPB, DIRECT, false>(a, stream);
+    a.out = part;
+    a.to_m = a.M;
+    a.to_n = a.N;
+    const hipError_t err = launch_product<DT, OPA, OPB, 64, 64, 2, 2, DIRECT ? 4 : 2, DIRECT, true>(a, stream);
+    if (err != hipSuccess) return err;
+    const uint64_t rows = (uint64_t)a.R * (uint64_t)a.M, threads = rows * (((uint32_t)a.N + 3) / 4);
+    hipLaunchKernelGGL((join_epilogue_kernel<DT>), grid_of_blocks((threads + kBlockThreads - 1) / kBlockThreads),
+                       dim3(kBlockThreads), 0, stream, part, plan.split, rows, a.M, a.N, a.e);
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -21,15 +21,20 @@ struct ProductPlan {
 
 inline long long tile_count(long long n, int tile) { return (n + tile - 1) / tile; }
 
-// Cost of `tiles` tiles in units of a tile of 256 that has a compute unit to itself. A
-// compute unit holds one workgroup of 256, two of 128 or four of 64.
+// Cost of `tiles` tiles in units of a round of tiles of 256, one on every compute unit
+// (K = 4096 bf16: 115 us). A compute unit holds one workgroup of 256, two of 128 or of 64
+// (four stages in LDS); alone on it, or with half of the device idle, they are faster.
+// Measured, us at K = N = 4096 and 64 / 512 / 768 / 1024 / 1536 / 2048 / 4096 rows: tiles of
+// 64 25 / 32 / 53 / 68 / 94 / 130 / 245, of 128 54 / 54 / 58 / 72 / 75 / 81 / 158, of 256
+// 86 / 88 / 97 / 108 / 112 / 112 / 115.
 inline double tile_cost(long long tiles, int tile, int cus) {
-    const int at_once = tile == kLargeTile ? 1 : tile == kMiddleTile ? 2 : 4;
-    const double one = tile == kLargeTile ? 1.0 : tile == kMiddleTile ? 0.34 : 0.16;     // alone on its compute unit
-    const double full = tile == kLargeTile ? 1.0 : tile == kMiddleTile ? 0.58 : 0.40;    // with the others beside it
-    const long long per = (tiles + cus - 1) / cus;       // of the fullest compute unit
-    const long long rounds = per / at_once, rest = per % at_once;
-    return (double)rounds * full + (rest ? one + (full - one) * (double)(rest - 1) / (double)(at_once - 1 ? at_once - 1 : 1) : 0.0);
+    const double one = tile == kLargeTile ? 0.75 : tile == kMiddleTile ? 0.47 : 0.22;    // half a round or less
+    const double full = tile == kLargeTile ? 1.0 : tile == kMiddleTile ? 0.69 : 0.275;   // a round
+    const long long round = tile == kLargeTile ? cus : 2 * cus;
+    const long long rounds = tiles / round, rest = tiles % round;
+    if (rest == 0) return (double)rounds * full;
+    const double part = 2.0 * (double)rest / (double)round - 1.0;   // beyond half a round
+    return (double)rounds * full + one + (part > 0.0 ? part * (full - one) : 0.0);
 }
 
 // large: tiles of 256 exist for the operands.
@@ -68,31 +73,56 @@ inline ProductPlan product_plan(long long batches, int M, int N, int cus, bool l
     return plan;
 }
 
-// How a weight gradient of R x H x K sums over T tokens runs. It goes by the sizes
-// alone, so that the workspace is the same on every device.
+// A sum over K in `split` runs of split_k (whole stages), none of them empty.
+struct SplitPlan {
+    int split, split_k;
+};
+
+inline SplitPlan split_runs(long long K, long long want) {
+    constexpr long long kStage = 64;
+    const long long stages = (K - 1) / kStage + 1;
+    // at least 8 stages to a run: a run costs a write and a read of the outputs
+    long long split = want < stages / 8 ? want : stages / 8;
+    if (split < 1) split = 1;
+    const long long run = (stages + split - 1) / split * kStage;
+    SplitPlan p;
+    p.split_k = (int)(run < K ? run : K);
+    p.split = (int)((K - 1) / run + 1);
+    return p;
+}
+
+// Linear layers and input gradients of few outputs: sums over K are split where the
+// tiles of 64 would leave compute units idle. It goes by the sizes alone, so that the
+// workspace (binary32 [split][batches][M][N]) is the same on every device.
+inline SplitPlan linear_plan(long long batches, int M, int N, int K) {
+    constexpr long long kFill = 512;   // tiles of 64 that fill the device, two on a compute unit
+    const long long tiles = batches * tile_count(M, kSmallTile) * tile_count(N, kSmallTile);
+    return split_runs(K, tiles <= kFill / 2 ? kFill / tiles : 1);
+}
+
+// How a weight gradient of R x H x K sums over T tokens runs, by the sizes alone too.
 struct WeightGradPlan {
     size_t value_bytes;   // of the activations as 16-bit values, 0: codes are read by the product
     size_t part_bytes;    // of the splits' sums (after the values), 0: one split
-    int split, split_k;   // tokens in `split` runs of split_k, none of them empty
+    SplitPlan split;
 };
 
 inline WeightGradPlan weight_grad_plan(int R, int T, int K, int H) {
-    constexpr long long kStage = 64, kFill = 512;   // tokens of a stage; tiles of 128 that fill the device
+    constexpr long long kFill = 512;   // tiles of 128 that fill the device, two on a compute unit
     WeightGradPlan p = {};
     const double work = (double)R * (double)T * (double)K * (double)H;
     if (H >= 1024 && H % 8 == 0 && work >= 1.5e10)
         p.value_bytes = ((size_t)R * (size_t)T * (size_t)K * 2 + 255) / 256 * 256;
-    const long long stages = (T - 1) / kStage + 1;
     const long long tiles = R * tile_count(H, kMiddleTile) * tile_count(K, kMiddleTile);
-    // at least 8 stages to a split: a part costs a write and a read of the outputs
-    long long split = tiles < kFill / 2 ? kFill / tiles : 1;
-    if (split > stages / 8) split = stages / 8;
-    if (split < 1) split = 1;
-    const long long run = (stages + split - 1) / split;
-    p.split_k = (int)(run * kStage < T ? run * kStage : T);
-    p.split = (int)((T - 1) / (run * kStage) + 1);
-    if (p.split > 1) p.part_bytes = (size_t)p.split * (size_t)R * (size_t)H * (size_t)K * 4;
+    p.split = split_runs(T, tiles < kFill / 2 ? kFill / tiles : 1);
+    if (p.split.split > 1) p.part_bytes = (size_t)p.split.split * (size_t)R * (size_t)H * (size_t)K * 4;
     return p;
 }
+
+// Tokens up to which a linear layer runs without LDS stages, its weights streamed
+// through the registers (fc_linear_act.hip); us at 1 / 4 / 8 / 16 tokens, streamed against
+// tiles: K = 8192, H = 7168 27 / 30 / 33 / 37 against 33 / 33 / 33 / 32; four ranks of
+// K = 2048, H = 8192 28 / 30 / 33 / 40 against 32 / 32 / 32 / 33.
+constexpr int kFewTokens = 8;
 
 }  // namespace fc

@@ -242,9 +242,22 @@ fc_status fc_activation_backward(const void *dy, const uint8_t *codes, const uin
     return from_hip(fc::launch_activation_backward(a, (int)dt, stream_of(stream)));
 }
 
+size_t fc_linear_act_workspace_bytes(int R, int T, int K, int H) {
+    if (check_product(R, T, K, H) != FC_OK || T <= fc::kFewTokens) return 0;
+    const int split = fc::linear_plan(R, T, H, K).split;
+    return split > 1 ? (size_t)split * elems(R, T, H) * 4 : 0;
+}
+
+size_t fc_linear_input_grad_workspace_bytes(int R, int T, int K, int H) {
+    if (check_product(R, T, K, H) != FC_OK || T == 0) return 0;
+    const int split = fc::linear_plan(R, T, K, H).split;
+    return split > 1 ? (size_t)split * elems(R, T, K) * 4 : 0;
+}
+
 fc_status fc_linear_act(const void *a, const void *w, fc_dtype dt, int R, int T, int K, int H,
                         const void *bias, fc_act act, const void *mul, const void *residual,
-                        void *y, void *z_out, void *stream) {
+                        void *y, void *z_out, void *workspace, size_t workspace_bytes,
+                        void *stream) {
     fc_status st = check_product(R, T, K, H);
     if (st != FC_OK) return st;
     if (act < FC_ACT_NONE || act > FC_ACT_GELU_TANH) return FC_ERR_VALUE;
@@ -253,11 +266,15 @@ fc_status fc_linear_act(const void *a, const void *w, fc_dtype dt, int R, int T,
     const size_t n = elems(R, T, H) * 2;
     const Span as = {a, elems(R, T, K) * 2}, ws = {w, elems(R, H, K) * 2}, bs = {bias, elems(R, 1, H) * 2},
                ms = {mul, n}, rs = {residual, n}, ys = {y, n}, zs = {z_out, n};
-    st = check_spans({as, ws, ys}, {bs, ms, rs, zs});
+    const size_t need = fc_linear_act_workspace_bytes(R, T, K, H);
+    if (need != 0 && workspace == nullptr) return FC_ERR_NULL;
+    const Span wk = {workspace, need};
+    st = check_spans({as, ws, ys}, {bs, ms, rs, zs, wk});
     if (st != FC_OK) return st;
-    st = check_overlap({ys, zs}, {as, ws, bs, ms});
+    if (workspace_bytes < need) return FC_ERR_WORKSPACE;
+    st = check_overlap({ys, zs, wk}, {as, ws, bs, ms});
     if (st != FC_OK) return st;
-    if ((y != residual && overlap(ys, rs)) || overlap(zs, rs)) return FC_ERR_OVERLAP;
+    if ((y != residual && overlap(ys, rs)) || overlap(zs, rs) || overlap(wk, rs)) return FC_ERR_OVERLAP;
     fc::LinearEpilogue e = {};
     e.bias = u16(bias);
     e.mul = u16(mul);
@@ -265,23 +282,29 @@ fc_status fc_linear_act(const void *a, const void *w, fc_dtype dt, int R, int T,
     e.y = u16(y);
     e.z = u16(z_out);
     e.act = (int)act;
-    return from_hip(fc::launch_linear_act(u16(a), u16(w), (int)dt, R, T, K, H, e, stream_of(stream)));
+    return from_hip(fc::launch_linear_act(u16(a), u16(w), (int)dt, R, T, K, H, e, workspace, stream_of(stream)));
 }
 
 fc_status fc_linear_input_grad(const void *dy, const void *w, fc_dtype dt, int R, int T, int K,
-                               int H, const void *residual, void *dx, void *stream) {
+                               int H, const void *residual, void *dx, void *workspace,
+                               size_t workspace_bytes, void *stream) {
     fc_status st = check_product(R, T, K, H);
     if (st != FC_OK) return st;
     if (!dtype_ok(dt)) return FC_ERR_DTYPE;
     if (T == 0) return FC_OK;
     const size_t n = elems(R, T, K) * 2;
     const Span ds = {dy, elems(R, T, H) * 2}, ws = {w, elems(R, H, K) * 2}, rs = {residual, n}, xs = {dx, n};
-    st = check_spans({ds, ws, xs}, {rs});
+    const size_t need = fc_linear_input_grad_workspace_bytes(R, T, K, H);
+    if (need != 0 && workspace == nullptr) return FC_ERR_NULL;
+    const Span wk = {workspace, need};
+    st = check_spans({ds, ws, xs}, {rs, wk});
     if (st != FC_OK) return st;
-    st = check_overlap({xs}, {ds, ws, dx == residual ? Span{nullptr, 0} : rs});
+    if (workspace_bytes < need) return FC_ERR_WORKSPACE;
+    st = check_overlap({xs, wk}, {ds, ws});
     if (st != FC_OK) return st;
+    if ((dx != residual && overlap(xs, rs)) || overlap(wk, rs)) return FC_ERR_OVERLAP;
     return from_hip(fc::launch_linear_input_grad(u16(dy), u16(w), (int)dt, R, T, K, H, u16(residual), u16(dx),
-                                                 stream_of(stream)));
+                                                 workspace, stream_of(stream)));
 }
 
 size_t fc_linear_weight_grad_workspace_bytes(int R, int T, int K, int H) {

@@ -98,11 +98,17 @@ size_t fc_layer_norm_backward_workspace_bytes(int T, int H);
  *   pass needs a payload of. bias, mul, residual and z_out are optional (NULL). y may
  *   be the same pointer as residual.
  * Any sizes with R, K, H >= 1, K, H <= 2^22 and R * ceil(T/16) * ceil(H/16) < 2^31;
- * rows that are whole 16-byte vectors (K % 8 == 0) are faster.
+ * rows that are whole 16-byte vectors (K % 8 == 0) are faster. workspace:
+ * fc_linear_act_workspace_bytes(R, T, K, H) bytes (0 and NULL allowed where the sums
+ * are not split); its contents afterwards are unspecified.
  */
 fc_status fc_linear_act(const void *a, const void *w, fc_dtype dt, int R, int T, int K, int H,
                         const void *bias, fc_act act, const void *mul, const void *residual,
-                        void *y, void *z_out, void *stream);
+                        void *y, void *z_out, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* 0 also where the arguments are unsupported. */
+size_t fc_linear_act_workspace_bytes(int R, int T, int K, int H);
 
 /*
  * The gradient of the layer's input: dx[r][t][k] = sum_h dy[r][t][h] * w[r][h][k] +
@@ -112,7 +118,11 @@ fc_status fc_linear_act(const void *a, const void *w, fc_dtype dt, int R, int T,
  *   residual. Sizes as for fc_linear_act.
  */
 fc_status fc_linear_input_grad(const void *dy, const void *w, fc_dtype dt, int R, int T, int K,
-                               int H, const void *residual, void *dx, void *stream);
+                               int H, const void *residual, void *dx, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* 0 also where the arguments are unsupported. */
+size_t fc_linear_input_grad_workspace_bytes(int R, int T, int K, int H);
 
 /*
  * The gradient of the weights, from the payload of the layer's input:
@@ -120,8 +130,9 @@ fc_status fc_linear_input_grad(const void *dy, const void *w, fc_dtype dt, int R
  *   dy [R][T][H] in dt, payload of [R][T][K] -> dw [R][H][K] binary32.
  * x is the payload's value rounded to dt (what fc_dequantize writes): the matrix
  * cores take 16-bit operands. Sizes as for fc_linear_act, K <= FC_TRAIN_MAX_ROW.
- * workspace: fc_linear_weight_grad_workspace_bytes(R, T, K, H) bytes (0 and NULL
- * allowed where the tokens are not split).
+ * workspace: fc_linear_weight_grad_workspace_bytes(R, T, K, H) bytes: the values as
+ * 16-bit ones for layers of many outputs, parts of the sums where few outputs sum over
+ * many tokens, else 0 (NULL allowed); its contents afterwards are unspecified.
  */
 fc_status fc_linear_weight_grad(const void *dy, const uint8_t *codes, const uint16_t *s,
                                 const uint16_t *z, int group, fc_dtype dt, int R, int T, int K,

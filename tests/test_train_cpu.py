@@ -91,8 +91,9 @@ def test_workspaces():
             f(*[2 ** 32 + 1] * n)
 
 
-def _linear(a=P(0), w=P(1), dt=0, R=2, T=8, K=128, H=64, bias=P(2), act=3, mul=P(3), res=P(4), y=P(5), z=P(6)):
-    return fc.lib().fc_linear_act(a, w, dt, R, T, K, H, bias, act, mul, res, y, z, None)
+def _linear(a=P(0), w=P(1), dt=0, R=2, T=8, K=128, H=64, bias=P(2), act=3, mul=P(3), res=P(4), y=P(5), z=P(6), ws=P(7),
+            nbytes=1 << 26):
+    return fc.lib().fc_linear_act(a, w, dt, R, T, K, H, bias, act, mul, res, y, z, ws, nbytes, None)
 
 
 @pytest.mark.parametrize("status,kw", [
@@ -109,8 +110,8 @@ def test_linear_act_refuses(status, kw):
     assert _linear(**kw) == status
 
 
-def _input_grad(dy=P(0), w=P(1), dt=0, R=2, T=8, K=128, H=64, res=P(2), dx=P(3)):
-    return fc.lib().fc_linear_input_grad(dy, w, dt, R, T, K, H, res, dx, None)
+def _input_grad(dy=P(0), w=P(1), dt=0, R=2, T=8, K=128, H=64, res=P(2), dx=P(3), ws=P(4), nbytes=1 << 26):
+    return fc.lib().fc_linear_input_grad(dy, w, dt, R, T, K, H, res, dx, ws, nbytes, None)
 
 
 @pytest.mark.parametrize("status,kw", [
@@ -120,6 +121,22 @@ def _input_grad(dy=P(0), w=P(1), dt=0, R=2, T=8, K=128, H=64, res=P(2), dx=P(3))
 ])
 def test_input_grad_refuses(status, kw):
     assert _input_grad(**kw) == status
+
+
+def test_products_workspaces_are_checked():
+    """Sums that are split: few outputs of long rows."""
+    for call, size, at in ((_linear, fc.fc_linear_act_workspace_bytes, 5), (_input_grad, fc.fc_linear_input_grad_workspace_bytes, 3)):
+        kw = dict(R=1, T=40, K=4096, H=128) if call is _linear else dict(R=1, T=40, K=128, H=4096)
+        need = size(**kw)
+        assert need > 0 and need % (40 * 128 * 4) == 0
+        assert call(**kw, nbytes=need - 1) == 5
+        assert call(**kw, ws=None) == 1
+        assert call(**kw, ws=P(7, 8)) == 4
+        for other in (0, 1, at):
+            assert call(**kw, ws=P(other)) == 9
+        assert call(**kw, ws=P(4 if call is _linear else 2)) == 9        # the residual
+        assert size(1, 8192, 4096, 4096) == 0 and size(1, 0, 4096, 4096) == 0 and size(1, 1, 1 << 23, 8) == 0
+    assert fc.fc_linear_act_workspace_bytes(1, 1, 4096, 64) == 0             # single tokens have none
 
 
 def _weight_grad(dy=P(0), codes=P(1), s=P(2), z=P(3), group=32, dt=0, R=2, T=8, K=128, H=64, acc=0, dw=P(4), ws=P(5), nbytes=0):
