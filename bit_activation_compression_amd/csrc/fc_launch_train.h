@@ -43,7 +43,7 @@ struct LayerNormBackArgs {
     float *part;
     float inv_h;
     int T, H;
-    int groups, waves, llog, grid;   // set by the launcher
+    int groups, waves, llog, teams, grid;   // set by the launcher
     uint32_t gmagic;
 };
 int layer_norm_parts(int T, int H);

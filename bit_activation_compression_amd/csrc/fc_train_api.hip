@@ -12,30 +12,46 @@
 namespace fc {
 namespace {
 
-constexpr int kSumWaves = 16;
+constexpr int kSumWaves = 16, kSumCols = 16, kSumRows = kSumWaves * (kWave / kSumCols);
 
-// A workgroup sums 64 columns of one rank: its waves take every 16th row each, and
-// their sums meet in LDS in the order of the waves. The rows are the workgroups'
-// sums of an earlier launch, mostly still in the L2 or the Infinity Cache.
+// A workgroup sums 16 columns of one rank: each 16 lanes take every 64th row, and their
+// sums meet in LDS, in a fixed order. The rows are the workgroups' sums of an earlier
+// launch, mostly still in the L2 or the Infinity Cache: this is bound by latency, and
+// has as many loads in flight as there are rows.
 __global__ __launch_bounds__(kSumWaves * kWave) void column_sum_kernel(const float *part, int parts, int stride, int cols,
                                                                        int split, int blocks, uint64_t total,
                                                                        float *out, float *out2) {
-    __shared__ float lds[kSumWaves][kWave];
-    const uint32_t thread = __builtin_amdgcn_workitem_id_x(), lane = thread & (kWave - 1), wave = thread / kWave;
+    __shared__ float lds[kSumRows][kSumCols];
+    const uint32_t thread = __builtin_amdgcn_workitem_id_x(), lane = thread % kSumCols, first = thread / kSumCols;
     const uint64_t id = grid_index();
     if (id >= total) return;
     const uint64_t r = id / (uint32_t)blocks;
-    const int c = (int)(id - r * (uint32_t)blocks) * kWave + (int)lane;
+    const int c = (int)(id - r * (uint32_t)blocks) * kSumCols + (int)lane;
     float s = 0.0f;
     if (c < cols) {
         const float *p = part + r * (uint64_t)parts * (uint32_t)stride + (uint32_t)c;
-        for (uint32_t i = wave; i < (uint32_t)parts; i += kSumWaves) s += p[(uint64_t)i * (uint32_t)stride];
-    }
-    lds[wave][lane] = s;
-    __syncthreads();
-    if (wave != 0 || c >= cols) return;
+        for (uint32_t i = first; i < (uint32_t)parts; i += kSumRows * 4) {
+            float v[4];
 #pragma unroll
-    for (int w = 1; w < kSumWaves; ++w) s += lds[w][lane];
+            for (uint32_t k = 0; k < 4; ++k) {
+                const uint32_t row = i + k * kSumRows;
+                v[k] = row < (uint32_t)parts ? p[(uint64_t)row * (uint32_t)stride] : 0.0f;
+            }
+            s += (v[0] + v[1]) + (v[2] + v[3]);
+        }
+    }
+    lds[first][lane] = s;
+    __syncthreads();
+    if (thread >= kWave) return;
+    // 4 lanes to a column, 16 rows each
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSumRows / 4; ++i) s += lds[first * (kSumRows / 4) + i][lane];
+    s += __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, s), 0x401F));   // lane ^ 16
+    const uint32_t bits = __builtin_bit_cast(uint32_t, s);
+    const auto halves = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);                     // lane ^ 32
+    s = __builtin_bit_cast(float, (uint32_t)halves[0]) + __builtin_bit_cast(float, (uint32_t)halves[1]);
+    if (thread >= kSumCols || c >= cols) return;
     if (c < split) out[r * (uint32_t)split + (uint32_t)c] = s;
     else out2[r * (uint32_t)(cols - split) + (uint32_t)(c - split)] = s;
 }
@@ -49,7 +65,7 @@ __global__ __launch_bounds__(kBlockThreads) void fill_zero_kernel(float *out, ui
 
 hipError_t launch_column_sum(const float *part, int R, int parts, int stride, int cols, int split, float *out,
                              float *out2, hipStream_t stream) {
-    const int blocks = (cols + kWave - 1) / kWave;
+    const int blocks = (cols + kSumCols - 1) / kSumCols;
     const uint64_t total = (uint64_t)R * (uint64_t)blocks;
     hipLaunchKernelGGL(column_sum_kernel, grid_of_blocks(total), dim3(kSumWaves * kWave), 0, stream, part, parts, stride,
                        cols, split, blocks, total, out, out2);
