@@ -44,6 +44,7 @@ constexpr uint32_t kRawBuffer = 0x00020000;         // resource word 3: raw 32-b
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
@@ -316,27 +317,39 @@ __device__ __forceinline__ void widen4(const uint16_t *p, int n, float (&v)[4]) 
     }
 }
 
+// Two binary32 values rounded to the dtype, the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+    const f32x2 pair = {as_f32(a), as_f32(b)};
+    if constexpr (DT == 1) return __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, bf16x2));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, f16x2));
+}
+
 template <int DT>
 __device__ __forceinline__ void store4(uint16_t *p, int n, const float (&v)[4]) {
-    uint16_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = narrow1<DT>(v[i]);
+    const uint32_t lo = narrow2<DT>(v[0], v[1]), hi = narrow2<DT>(v[2], v[3]);
     if (n >= 4) {
-        *reinterpret_cast<u32x2_a2 *>(p) = u32x2{(uint32_t)h[0] | (uint32_t)h[1] << 16, (uint32_t)h[2] | (uint32_t)h[3] << 16};
+        *reinterpret_cast<u32x2_a2 *>(p) = u32x2{lo, hi};
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) p[i] = h[i];
+        for (int i = 0; i < 3; ++i)
+            if (i < n) p[i] = (uint16_t)((i < 2 ? lo : hi) >> (16 * (i & 1)));
     }
 }
 
-__device__ __forceinline__ float activate(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ void activate4(float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_value<ACT>(v[i]);
+}
+
+__device__ __forceinline__ void activate4(float (&v)[4], int act) {
     switch (act) {
-    case kActRelu: return act_value<kActRelu>(z);
-    case kActSilu: return act_value<kActSilu>(z);
-    case kActGelu: return act_value<kActGelu>(z);
-    case kActGeluTanh: return act_value<kActGeluTanh>(z);
-    default: return z;
+    case kActRelu: activate4<kActRelu>(v); break;
+    case kActSilu: activate4<kActSilu>(v); break;
+    case kActGelu: activate4<kActGelu>(v); break;
+    case kActGeluTanh: activate4<kActGeluTanh>(v); break;
+    default: break;
     }
 }
 
@@ -352,10 +365,7 @@ __device__ __forceinline__ void finish4(const LinearEpilogue &e, uint64_t at, in
         for (int i = 0; i < 4; ++i) v[i] += bias[i];
     }
     if (e.z != nullptr) store4<DT>(e.z + at, left, v);
-    if (e.act != kActNone) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = activate(v[i], e.act);
-    }
+    activate4(v, e.act);
     if (e.mul != nullptr) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] *= m[i];
@@ -390,7 +400,7 @@ template <int DT, int OPA, int OPB, int TM, int TN, int WM, int WN, int NS, bool
 __global__ __launch_bounds__((Shape<TM, TN, WM, WN, NS>::kThreads)) __attribute__((amdgpu_waves_per_eu(Shape<TM, TN, WM, WN, NS>::kPerSimd)))
 void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
     using S = Shape<TM, TN, WM, WN, NS>;
-    constexpr int kLds = S::kRing > S::kEpilogue || F32 ? S::kRing : S::kEpilogue;
+    constexpr int kLds = S::kRing > S::kEpilogue ? S::kRing : S::kEpilogue;
     __shared__ __attribute__((aligned(16))) uint8_t shared[kLds];
     uint8_t FC_LDS *lds = (uint8_t FC_LDS *)shared;
     const uint32_t tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63u;
@@ -560,52 +570,43 @@ void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
         here = next;
     }
 
-    if constexpr (F32) {
-        float *out = a.out + (uint64_t)batch * ((uint64_t)a.M * (uint32_t)a.N);
+    // 32 rows of the wave at a time through its own part of LDS, from where a lane takes 4
+    // neighbouring columns of a row: whole lines go out
+    constexpr int kLanesRow = S::kSN / 4, kRowsTurn = kWave / kLanesRow;
+    meet();   // every wave has read its last fragments
+    FC_LDS float *mine = (FC_LDS float *)(lds) + wave * 32 * S::kPitch;
+    const int c = (int)(lane % kLanesRow) * 4, n = n0 + wn * S::kSN + c, left = a.N - n;
+    float bias[4] = {};
+    if (!F32 && a.e.bias != nullptr && left > 0) widen4<DT>(a.e.bias + (uint64_t)r * (uint32_t)a.N + (uint32_t)n, left, bias);
 #pragma unroll
-        for (int i = 0; i < S::kBM; ++i)
+    for (int i = 0; i < S::kBM; i += 2) {
 #pragma unroll
-            for (int j = 0; j < S::kBN; ++j) {
-                const int n = n0 + wn * S::kSN + j * kBlock + (int)(lane & 15u);
-                const int mb = m0 + wm * S::kSM + i * kBlock + (int)(lane >> 4) * 4;
-                if (n < a.N) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const int m = mb + v;
-                        if (m < a.M) {
-                            float *o = out + (uint64_t)(uint32_t)m * (uint32_t)a.N + (uint32_t)n;
-                            *o = a.accumulate ? *o + acc[i][j][v] : acc[i][j][v];
-                        }
-                    }
+            for (int j = 0; j < S::kBN; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    mine[(h * kBlock + 4 * (lane >> 4) + v) * S::kPitch + j * kBlock + (lane & 15u)] = acc[i + h][j][v];
+        for (int t = 0; t < 32; t += kRowsTurn) {
+            const int row = t + (int)(lane / kLanesRow), m = m0 + wm * S::kSM + i * kBlock + row;
+            const f32x4 w = *(const FC_LDS f32x4 *)(mine + row * S::kPitch + c);
+            float v[4] = {w.x, w.y, w.z, w.w};
+            if (m >= a.M || left <= 0) continue;
+            if constexpr (F32) {
+                float *o = a.out + ((uint64_t)batch * (uint32_t)a.M + (uint32_t)m) * (uint32_t)a.N + (uint32_t)n;
+                if (left >= 4) {
+                    f32x4_a4 *q = reinterpret_cast<f32x4_a4 *>(o);
+                    f32x4_a4 sum = {v[0], v[1], v[2], v[3]};
+                    if (a.accumulate) sum += *q;
+                    *q = sum;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        if (k < left) o[k] = a.accumulate ? o[k] + v[k] : v[k];
                 }
+            } else {
+                finish4<DT>(a.e, ((uint64_t)r * (uint32_t)a.M + (uint32_t)m) * (uint32_t)a.N + (uint32_t)n, left, bias, v);
             }
-    } else {
-        // 32 rows of the wave at a time through its own part of LDS, from where a lane
-        // takes 4 neighbouring columns of a row
-        constexpr int kLanesRow = S::kSN / 4, kRowsTurn = kWave / kLanesRow;
-        meet();   // every wave has read its last fragments
-        FC_LDS float *mine = (FC_LDS float *)(lds) + wave * 32 * S::kPitch;
-        const int c = (int)(lane % kLanesRow) * 4, n = n0 + wn * S::kSN + c, left = a.N - n;
-        float bias[4] = {};
-        if (a.e.bias != nullptr && left > 0) widen4<DT>(a.e.bias + (uint64_t)r * (uint32_t)a.N + (uint32_t)n, left, bias);
-#pragma unroll
-        for (int i = 0; i < S::kBM; i += 2) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < S::kBN; ++j)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        mine[(h * kBlock + 4 * (lane >> 4) + v) * S::kPitch + j * kBlock + (lane & 15u)] = acc[i + h][j][v];
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            for (int t = 0; t < 32; t += kRowsTurn) {
-                const int row = t + (int)(lane / kLanesRow), m = m0 + wm * S::kSM + i * kBlock + row;
-                const f32x4 w = *(const FC_LDS f32x4 *)(mine + row * S::kPitch + c);
-                float v[4] = {w.x, w.y, w.z, w.w};
-                if (m < a.M && left > 0)
-                    finish4<DT>(a.e, ((uint64_t)r * (uint32_t)a.M + (uint32_t)m) * (uint32_t)a.N + (uint32_t)n, left, bias, v);
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
     }
 }
