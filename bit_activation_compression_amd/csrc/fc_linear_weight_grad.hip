@@ -21,8 +21,14 @@ hipError_t run(const ProductArgs &a, hipStream_t stream) {
 __global__ __launch_bounds__(kBlockThreads) void join_kernel(const float *part, int split, uint64_t n, int accumulate, float *dw) {
     const uint64_t i = grid_index() * kBlockThreads + __builtin_amdgcn_workitem_id_x();
     if (i >= n) return;
-    float s = part[i];
-    for (int p = 1; p < split; ++p) s += part[(uint64_t)p * n + i];
+    float s = 0.0f;
+    for (int p = 0; p < split; p += 8) {   // 8 loads in flight at a time
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = p + k < split ? part[(uint64_t)(p + k) * n + i] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += v[k];
+    }
     dw[i] = accumulate ? dw[i] + s : s;
 }
 

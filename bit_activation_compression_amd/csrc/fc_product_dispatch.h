@@ -101,6 +101,12 @@ inline SplitPlan linear_plan(long long batches, int M, int N, int K) {
 }
 
 // How a weight gradient of R x H x K sums over T tokens runs, by the sizes alone too.
+// Codes that many rows of tiles would each turn into values are turned into them once,
+// before the product; us with the codes read by the product against values first, T x K x
+// H: 8192 x 4096 x 512 92 against 80, 2048 x 4096 x 1024 61 against 43, 256 x 4096 x 4096
+// 32 against 25, four ranks of 512 x 1024 x 1024 20 against 17; 1024^3 16 against 16, 16 x
+// 4096 x 4096 18 against 19; few rows of tiles: 8192 x 4096 x 64 26 against 47, 65536 x 256
+// x 256 37 against 42.
 struct WeightGradPlan {
     size_t value_bytes;   // of the activations as 16-bit values, 0: codes are read by the product
     size_t part_bytes;    // of the splits' sums (after the values), 0: one split
@@ -111,7 +117,7 @@ inline WeightGradPlan weight_grad_plan(int R, int T, int K, int H) {
     constexpr long long kFill = 512;   // tiles of 128 that fill the device, two on a compute unit
     WeightGradPlan p = {};
     const double work = (double)R * (double)T * (double)K * (double)H;
-    if (H >= 1024 && H % 8 == 0 && work >= 1.5e10)
+    if (H >= 512 && H % 8 == 0 && work >= 1e9)
         p.value_bytes = ((size_t)R * (size_t)T * (size_t)K * 2 + 255) / 256 * 256;
     const long long tiles = R * tile_count(H, kMiddleTile) * tile_count(K, kMiddleTile);
     p.split = split_runs(T, tiles < kFill / 2 ? kFill / tiles : 1);
