@@ -17,13 +17,11 @@ constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTa
 
 __device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
 
-// p = 1 / (1 + exp(-v)) and q = 1 - p, both to their own last digits.
+// p = 1 / (1 + exp(-v)), to its own last digits also where it is small, and q = 1 - p,
+// to the last digits of 1: what it is multiplied with is small where it vanishes.
 __device__ __forceinline__ void sigmoid_pair(float v, float &p, float &q) {
-    const float e = exp_of(-__builtin_fabsf(v));
-    const float r = __builtin_amdgcn_rcpf(1.0f + e), l = e * r;
-    const bool neg = v < 0.0f;
-    p = neg ? l : r;
-    q = neg ? r : l;
+    p = __builtin_amdgcn_rcpf(1.0f + exp_of(-v));
+    q = 1.0f - p;
 }
 
 // Phi(z), and exp(-z^2 / 2)

@@ -8,7 +8,7 @@
 // that db needs no exchange until the share's end: the workgroup's rows meet in
 // LDS, and a second launch adds the shares in a fixed order. Each operand is read
 // once and each output written once: 5 bytes per element (8 with mul), bound by
-// memory.
+// memory: 8192 x 7168 with mul 89 us, 5.3 TB/s; without 55, 5.4; GELU with db 68, 4.4.
 #include "fc_act.h"
 #include "fc_grid.h"
 #include "fc_launch_train.h"
@@ -20,6 +20,8 @@ namespace {
 constexpr int kShareThreads = 256;   // of a workgroup with a share of the rows
 constexpr int kWholeThreads = 1024;  // of one that has all rows of its columns
 constexpr int kBlocks = 2048;        // workgroups of shares that fill the device
+constexpr int kAhead = 2;            // rows of a lane in flight
+constexpr int kFree = 16384;         // without sums (8192 x 7168, SiLU and mul: 89 us, with 2048 99)
 
 template <int DT, int ACT, bool MUL, bool SUMS, int kThreads>
 __global__ __launch_bounds__(kThreads) void activation_back_kernel(const ActBackArgs a) {
@@ -35,26 +37,49 @@ __global__ __launch_bounds__(kThreads) void activation_back_kernel(const ActBack
     const int e = ((int)(cb << a.clog) + lane) * kLaneElems;
     const int last = H > kLaneElems ? H - kLaneElems : 0, b = e < last ? e : last;
     const bool live = e < H;
-    const int64_t first = (int64_t)part * a.chunk;
-    const int64_t end = first + a.chunk < a.T ? first + a.chunk : a.T;
+    // share `part` has every parts-th turn of rows: the workgroups that run at a time
+    // read neighbouring rows (8192 x 7168 with GELU and db 68 us, with shares of
+    // consecutive rows 73)
+    const int64_t first = (int64_t)part * rows, step = (int64_t)a.parts * rows, end = a.T;
     float db[kLaneElems] = {};
     uint32_t g = 0;
     if constexpr (ACT != kActNone) g = group_of((uint32_t)b / kLaneElems, a.gmagic);
     if (live) {
-        for (int64_t t = first + (thread >> a.clog); t < end; t += rows) {
+        // a row's operands, as loaded
+        struct Row {
+            u32x4 dy;
+            u32x2 qz, qm;
+            uint16_t zs, zz, ms, mz;
+        };
+        auto load = [&](int64_t t, Row &o) {
             const uint64_t row = (uint64_t)r * (uint32_t)a.T + (uint64_t)t, at = row * (uint64_t)H;
-            float dy[kLaneElems];
-            widen8<DT>(load_row8(a.dy + at, b, H), dy);
-            if constexpr (ACT != kActNone) {
+            if constexpr (ACT == kActNone) {
+                o.dy = load_row8(a.dy + at, b, H);
+            } else {
+                // rows are whole vectors: groups are multiples of 8
                 const uint64_t go = row * (uint64_t)a.groups + g;
-                const u32x2 qz = *reinterpret_cast<const u32x2 *>(a.pz.codes + at + (uint32_t)b);
-                const uint32_t wz[2] = {qz.x, qz.y};
-                float z[kLaneElems], m[kLaneElems], dm[kLaneElems];
-                dequant8<8>(wz, a.pz.s[go], a.pz.z[go], z);
+                o.dy = *reinterpret_cast<const u32x4 *>(a.dy + at + (uint32_t)b);
+                o.qz = *reinterpret_cast<const u32x2 *>(a.pz.codes + at + (uint32_t)b);
+                o.zs = a.pz.s[go];
+                o.zz = a.pz.z[go];
                 if constexpr (MUL) {
-                    const u32x2 qm = *reinterpret_cast<const u32x2 *>(a.pm.codes + at + (uint32_t)b);
-                    const uint32_t wm[2] = {qm.x, qm.y};
-                    dequant8<8>(wm, a.pm.s[go], a.pm.z[go], m);
+                    o.qm = *reinterpret_cast<const u32x2 *>(a.pm.codes + at + (uint32_t)b);
+                    o.ms = a.pm.s[go];
+                    o.mz = a.pm.z[go];
+                }
+            }
+        };
+        auto finish = [&](int64_t t, const Row &o) {
+            const uint64_t at = ((uint64_t)r * (uint32_t)a.T + (uint64_t)t) * (uint64_t)H;
+            float dy[kLaneElems];
+            widen8<DT>(o.dy, dy);
+            if constexpr (ACT != kActNone) {
+                const uint32_t wz[2] = {o.qz.x, o.qz.y};
+                float z[kLaneElems], m[kLaneElems], dm[kLaneElems];
+                dequant8<8>(wz, o.zs, o.zz, z);
+                if constexpr (MUL) {
+                    const uint32_t wm[2] = {o.qm.x, o.qm.y};
+                    dequant8<8>(wm, o.ms, o.mz, m);
                 }
 #pragma unroll
                 for (int k = 0; k < kLaneElems; ++k) {
@@ -71,6 +96,20 @@ __global__ __launch_bounds__(kThreads) void activation_back_kernel(const ActBack
 #pragma unroll
                 for (int k = 0; k < kLaneElems; ++k) db[k] += dy[k];
             }
+        };
+        // kAhead rows in flight at a time
+        int64_t t = first + (thread >> a.clog);
+        for (; t + (kAhead - 1) * step < end; t += kAhead * step) {
+            Row row[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) load(t + i * step, row[i]);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) finish(t + i * step, row[i]);
+        }
+        for (; t < end; t += step) {
+            Row row;
+            load(t, row);
+            finish(t, row);
         }
     }
     if constexpr (SUMS) {
@@ -90,29 +129,22 @@ __global__ __launch_bounds__(kThreads) void activation_back_kernel(const ActBack
 }
 
 // Rows up to which one workgroup sums all of them, 64 or more at a time, for 128
-// columns: one launch and no workspace (100 rows of 3584 with db: 5.6 us against 8.5 in
-// two launches).
-constexpr int kWholeRows = 256;
+// columns: one launch and no workspace. Rows of 3584 with GELU and db: 100 of them 6.0 us,
+// 256 10.3; 256 in shares and two launches 7.6.
+constexpr int kWholeRows = 128;
 
-// Lanes of a row's vectors, workgroups across a row, and shares of the rows: as many as
-// fill the device, each of whole turns of the workgroup's rows.
-void plan(int R, int T, int H, bool whole, int &clog, int &blocks, int &parts, int &chunk) {
+// Lanes of a row's vectors, workgroups across a row, and shares of the rows' turns: as
+// many as fill the device.
+void plan(int R, int T, int H, bool whole, int fill, int &clog, int &blocks, int &parts) {
     const int nv = (H + kLaneElems - 1) / kLaneElems;
     const int most = whole ? 16 : kWave;
     clog = lanes_log(nv < most ? nv : most);
     blocks = (nv + (1 << clog) - 1) >> clog;
-    if (whole) {
-        parts = 1;
-        chunk = T;
-        return;
-    }
     const int rows = kShareThreads >> clog;
     const long long turns = ((long long)T + rows - 1) / rows;
-    long long want = kBlocks / ((long long)R * blocks);
+    long long want = fill / ((long long)R * blocks);
     want = want < 1 ? 1 : want > turns ? turns : want;
-    const long long per = want > 0 ? (turns + want - 1) / want : 1;
-    parts = turns > 0 ? (int)((turns + per - 1) / per) : 1;
-    chunk = (int)(per * rows < T ? per * rows : T);
+    parts = whole ? 1 : (int)want;
 }
 
 template <int DT, int ACT, bool MUL>
@@ -143,14 +175,14 @@ hipError_t by_act(const ActBackArgs &a, hipStream_t stream) {
 }  // namespace
 
 int activation_parts(int R, int T, int H) {
-    int clog, blocks, parts, chunk;
-    plan(R, T, H, T <= kWholeRows, clog, blocks, parts, chunk);
+    int clog, blocks, parts;
+    plan(R, T, H, T <= kWholeRows, kBlocks, clog, blocks, parts);
     return parts;
 }
 
 hipError_t launch_activation_backward(const ActBackArgs &args, int dtype, hipStream_t stream) {
     ActBackArgs a = args;
-    plan(a.R, a.T, a.H, a.db != nullptr && a.T <= kWholeRows, a.clog, a.blocks, a.parts, a.chunk);
+    plan(a.R, a.T, a.H, a.db != nullptr && a.T <= kWholeRows, a.db != nullptr ? kBlocks : kFree, a.clog, a.blocks, a.parts);
     if (a.act == kActNone) {
         // dy's column sums alone
         return dtype == 0 ? launch_act<0, kActNone, false>(a, stream) : launch_act<1, kActNone, false>(a, stream);

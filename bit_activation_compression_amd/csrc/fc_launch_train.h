@@ -61,7 +61,7 @@ struct ActBackArgs {
     uint16_t *dz, *dmul;
     float *db, *part;
     int R, T, H;
-    int chunk, parts, clog, blocks, groups;   // set by the launcher
+    int parts, clog, blocks, groups;   // set by the launcher
     uint32_t gmagic;
 };
 int activation_parts(int R, int T, int H);

@@ -72,6 +72,49 @@ SHAPES = [(1, 1, 1, 1), (1, 1, 8, 16), (1, 1, 4096, 256), (2, 1, 100, 48), (1, 2
           (3, 300, 264, 520), (1, 1100, 56, 72), (1, 2050, 520, 300), (1, 1024, 1024, 2048), (1, 64, 8192, 64)]
 
 
+# (R, T, K, H) of the largest tiles: whole rounds of them, and columns or rows left to
+# smaller ones; ragged ones; a single stage, few and many; several ranks
+LARGE_SHAPES = [(1, 4096, 200, 4096), (1, 8192, 72, 2816), (1, 2816, 136, 8192), (2, 2050, 64, 4104), (1, 4000, 1032, 4100),
+                (4, 2048, 8, 2048), (1, 1500, 512, 4096), (1, 3300, 264, 3304)]
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("R,T,K,H", LARGE_SHAPES)
+def test_large_tiles(R, T, K, H, dt):
+    """The linear layer, and the input gradient of a layer of H inputs and K outputs."""
+    _say(f"large tiles {R}x{T}x{K}x{H} {dt}")
+    d = _layer(R, T, K, H, dt, T + K, bias=True, mul=False, skip=True)
+    _check_linear(d, "none", dt)
+    w = d["w"].transpose(-1, -2).contiguous()
+    dx = Guarded((R, T, H), dt)
+    fc.fc_linear_input_grad(_on(d["a"]), _on(w), residual=_on(d["residual"]), dx=dx.t)
+    want, bound = ref.product(d["a"].double(), w.double())
+    want = want + d["residual"].double()
+    ref.assert_within(dx.t, want, dt, bound + 4 * ref.U * (want.abs() + d["residual"].double().abs()), "dx")
+    dx.check()
+
+
+LARGE_WEIGHTS = [(200, 4096, 4096, 128), (72, 2816, 8192, 88), (130, 8192, 2816, 64), (65, 4104, 4096, 24), (40000, 64, 512, 64),
+                 (5000, 512, 520, 8), (300, 2048, 2048, 32), (9000, 1024, 300, 16), (9000, 1032, 304, 24)]
+
+
+@pytest.mark.parametrize("T,K,H,group", LARGE_WEIGHTS)
+def test_weight_grad_large_tiles(T, K, H, group):
+    """Many outputs: the values are made before the product, also from groups that are no
+    power of two; summed into a gradient as well."""
+    _say(f"weight grad large tiles {T}x{K}x{H} g={group}")
+    dy = torch.randn(1, T, H, generator=torch.Generator().manual_seed(T)).to(BF16)
+    payload = _payload(1, T, K, group, BF16, T)
+    args = (_on(dy), _on(payload))
+    dw = fc.fc_linear_weight_grad(*args)
+    x = ref.held(payload, group).float().to(BF16).double()
+    want, bound = ref.product(dy.double().transpose(-1, -2).contiguous(), x)
+    ref.assert_f32(dw, want, bound, "dw")
+    start = torch.randn(1, H, K, generator=torch.Generator().manual_seed(2))
+    summed = fc.fc_linear_weight_grad(*args, dw=start.cuda(), accumulate=True)
+    ref.assert_f32(summed, want + start.double(), bound + 2 * ref.U * (want.abs() + start.double().abs()), "dw summed")
+
+
 @pytest.mark.parametrize("dt", [BF16, F16])
 @pytest.mark.parametrize("R,T,K,H", SHAPES)
 def test_linear_shapes(R, T, K, H, dt):
@@ -132,7 +175,8 @@ def test_linear_nan_and_infinities_follow_the_formulas(T, K, H):
 
 GRAD_SHAPES = [(1, 1, 8, 8), (1, 1, 256, 512), (2, 3, 40, 24), (1, 16, 64, 1000), (1, 33, 72, 65), (3, 65, 128, 100),
                (1, 100, 264, 127), (1, 128, 256, 64), (2, 129, 136, 200), (1, 257, 520, 264), (1, 300, 1000, 33),
-               (1, 511, 64, 513), (1, 700, 768, 192), (1, 2000, 24, 16), (1, 1030, 1032, 520), (1, 130, 56, 2048)]
+               (1, 511, 64, 513), (1, 700, 768, 192), (1, 2000, 24, 16), (1, 1030, 1032, 520), (1, 130, 56, 2048),
+               (1, 1100, 1024, 1000)]
 
 
 @pytest.mark.parametrize("dt", [BF16, F16])
@@ -184,8 +228,10 @@ def test_weight_grad_shapes(i, dt):
     ref.assert_f32(summed, want + start.double(), bound + 2 * ref.U * (want.abs() + start.double().abs()), "dw summed")
 
 
-@pytest.mark.parametrize("T,K,H,group", [(5000, 64, 40, 8), (33000, 128, 72, 32), (20011, 520, 136, 104), (70001, 8, 8, 8),
-                                         (9000, 264, 129, 24)])
+LONG_SUMS = [(5000, 64, 40, 8), (33000, 128, 72, 32), (20011, 520, 136, 104), (70001, 8, 8, 8), (9000, 264, 129, 24)]
+
+
+@pytest.mark.parametrize("T,K,H,group", LONG_SUMS)
 def test_weight_grad_long_sums(T, K, H, group):
     """Few outputs and many tokens: the sums are split, and joined in a fixed order."""
     _say(f"weight grad T={T} {K}x{H} g={group}")
@@ -278,6 +324,134 @@ def test_no_tokens():
     db = torch.ones(2, 24, device="cuda")
     fc.fc_activation_backward(e(2, 0, 24), "silu", pay(2, 0, 24), db=db)
     assert (db == 0).all()
+
+
+# --- sizes past 32 bits and grids past 2^20 workgroups -------------------------
+
+def _codes(*shape, group):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    c = torch.randint(0, 256, shape, dtype=torch.uint8, device="cuda", generator=g)
+    s = (torch.rand(*shape[:-1], shape[-1] // group, device="cuda", generator=g) * 0.02 + 0.01).half()
+    return c, s.view(torch.uint16), (-128 * s).view(torch.uint16)
+
+
+def _big(*shape):
+    return torch.randn(shape, dtype=BF16, device="cuda", generator=torch.Generator(device="cuda").manual_seed(4))
+
+
+def test_operands_of_more_than_2_to_32_bytes():
+    """300000 rows of 8192, checked at both ends."""
+    T, H = 300000, 8192
+    ends = [slice(0, 3), slice(T - 5, T)]
+    x, w = _big(T, H), _big(H)
+    _say("large norm")
+    y, mean, rstd, payload = fc.fc_layer_norm(x, w, None, stats=True, group=512)
+    for e in ends:
+        r = ref.layer_norm(x[e].cpu().double(), w.cpu().double(), None, 1e-5, False)
+        ref.assert_within(y[e], r["y"], BF16, r["ey"], "y")
+        ref.assert_f32(rstd[e], r["rstd"], r["erstd"], "rstd")
+        ref.assert_f32(mean[e], r["mean"], r["emean"], "mean")
+        for got, want in zip(payload, ref.quantized(x[e].cpu(), 512)):
+            assert torch.equal(got[e].cpu().contiguous().view(torch.uint8), want.view(torch.uint8))
+    _say("large norm backward")
+    dx, dw, db = fc.fc_layer_norm_backward(y, payload, mean, rstd, w)
+    for e in ends:
+        held = ref.held(tuple(t[e].cpu().contiguous() for t in payload), 512)
+        r = ref.layer_norm_backward(y[e].cpu().double(), held, mean[e].cpu().double(), rstd[e].cpu().double(), w.cpu().double(), None)
+        ref.assert_within(dx[e], r["dx"], BF16, r["edx"], "dx")
+    for c in (0, H - 2):
+        n = ((payload[0][:, c:c + 2].double() * payload[1].view(torch.float16)[:, [c // 512]].double()
+              + payload[2].view(torch.float16)[:, [c // 512]].double()) - mean[:, None].double()) * rstd[:, None].double()
+        d = y[:, c:c + 2].double()
+        # each product is off by 4 roundings, the sum by its additions
+        bound = (ref.chain(T) + 4) * ref.U * (d * n).abs().sum(0) + 4 * ref.U * d.abs().sum(0)
+        assert ((dw[c:c + 2].double() - (d * n).sum(0)).abs() <= bound).all()
+        assert ((db[c:c + 2].double() - d.sum(0)).abs() <= ref.chain(T) * ref.U * d.abs().sum(0)).all()
+    del dx, x
+    _say("large activation backward")
+    dz, _, db = fc.fc_activation_backward(y, "relu", payload, bias=True)
+    for e in ends:
+        de = fc.fc_activation_backward(y[e].contiguous(), "relu", tuple(t[e].contiguous() for t in payload))[0]
+        assert torch.equal(dz[e], de)
+    del dz, payload
+    _say("large input grad")
+    w2, r2 = _big(64, H), _big(T, 64)
+    dx = fc.fc_linear_input_grad(r2, w2)
+    for e in ends:
+        assert torch.equal(dx[e], fc.fc_linear_input_grad(r2[e].contiguous(), w2))
+    del dx
+    _say("large linear")
+    a2 = _big(T, 64)
+    out, _ = fc.fc_linear_act(a2, w2.t().contiguous())
+    for e in ends:
+        # few tokens of 64 k: the same order of sums in both kernels
+        want = (a2[e].double() @ w2.double())
+        assert ((out[e].double() - want).abs() <= 2.0 ** -8 * want.abs() + 136 * ref.U * (a2[e].double().abs() @ w2.double().abs())).all()
+    del out
+    _say("large weight grad")
+    p = _codes(T, 64, group=32)
+    dw = fc.fc_linear_weight_grad(y, p)
+    v = fc.fc_dequantize(p[0], p[1], p[2], T, 64, 8, 32, BF16).double()
+    for e in (slice(0, 4), slice(H - 4, H)):
+        d = y[:, e].double().t().contiguous()
+        assert ((dw[e].double() - d @ v).abs() <= (2 * T + 8) * ref.U * (d.abs() @ v.abs())).all()
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_weights_of_more_than_2_to_32_bytes(T):
+    H, K = 300000, 8192
+    w, a = _big(H, K), _big(T, K)
+    _say(f"large weights T={T}")
+    y, _ = fc.fc_linear_act(a, w)
+    for e in (slice(0, 5), slice(H - 5, H)):
+        want, mag = a.double() @ w[e].double().t(), a.double().abs() @ w[e].double().abs().t()
+        assert ((y[:, e].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2 * K + 4) * ref.U * mag).all()
+
+
+def test_grids_of_more_than_2_to_20_workgroups():
+    R = (1 << 20) + 77
+    _say("many ranks, few tokens")
+    a, w = _big(R, 1, 8), _big(R, 16, 8)
+    y, _ = fc.fc_linear_act(a, w)
+    tail = slice(R - 100, R)
+    assert torch.equal(y[tail], fc.fc_linear_act(a[tail].clone(), w[tail].clone())[0])
+    _say("many ranks, input and weight gradients")
+    dy = _big(R, 9, 16)
+    dx = fc.fc_linear_input_grad(dy, w)
+    assert torch.equal(dx[tail], fc.fc_linear_input_grad(dy[tail].clone(), w[tail].clone()))
+    p = _codes(R, 9, 8, group=8)
+    dw = fc.fc_linear_weight_grad(dy, p)
+    assert torch.equal(dw[tail], fc.fc_linear_weight_grad(dy[tail].clone(), tuple(t[tail].clone() for t in p)))
+    _say("many ranks, activation backward")
+    dz, _, db = fc.fc_activation_backward(dx, "silu", p, bias=True)
+    dze, _, dbe = fc.fc_activation_backward(dx[tail].clone(), "silu", tuple(t[tail].clone() for t in p), bias=True)
+    assert torch.equal(dz[tail], dze) and torch.equal(db[tail], dbe)
+    _say("many rows of a norm")
+    for rows, H in ((R, 520), (4 * R, 512)):
+        x = _big(rows, H)
+        y = fc.fc_layer_norm(x)[0]
+        r = ref.layer_norm(x[-50:].cpu().double(), None, None, 1e-5, False)
+        ref.assert_within(y[-50:], r["y"], BF16, r["ey"], "y")
+
+
+def test_streams_do_not_share_workspaces():
+    """Split products, weight and bias gradients on two streams at once, many times."""
+    d = _layer(1, 40, 4096, 128, BF16, 21)
+    dy, p = _big(6000, 128), _codes(6000, 64, group=16)
+    calls = [lambda: fc.fc_linear_act(*(_on(d[k]) for k in ("a", "w", "bias")), "gelu")[0],
+             lambda: fc.fc_linear_weight_grad(dy, p), lambda: fc.fc_activation_backward(dy, "none", bias=True)[2]]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for turn in range(10):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append([c() for c in calls])
+    torch.cuda.synchronize()
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
 
 
 class _Block:
