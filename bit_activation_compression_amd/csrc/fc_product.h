@@ -554,7 +554,9 @@ void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
 #pragma unroll
     for (int p = 0; p < NS; ++p)
         if (p < stages) issue(p, (uint32_t)p * S::kStage, 0, 1);
-    if (!kThroughRegs && stages >= NS) wait_memory<(NS - 1) * kLoads>();
+    // every stage's loads have one prefetch behind them, which the waits below count
+    if constexpr (kPrefetch) prefetch(NS);
+    if (!kThroughRegs && stages >= NS) wait_memory<(NS - 1) * kLoads + (kPrefetch ? 1 : 0)>();
     else wait_memory<0>();
     meet();
 #pragma unroll
@@ -611,6 +613,7 @@ void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
     // 32 rows of the wave at a time through its own part of LDS, from where a lane takes 4
     // neighbouring columns of a row: whole lines go out
     constexpr int kLanesRow = S::kSN / 4, kRowsTurn = kWave / kLanesRow;
+    if constexpr (kPrefetch) wait_memory<0>();   // the last prefetch's store to LDS
     meet();   // every wave has read its last fragments
     FC_LDS float *mine = (FC_LDS float *)(lds) + wave * 32 * S::kPitch;
     const int c = (int)(lane % kLanesRow) * 4, n = n0 + wn * S::kSN + c, left = a.N - n;

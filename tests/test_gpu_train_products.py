@@ -94,6 +94,24 @@ def test_large_tiles(R, T, K, H, dt):
     dx.check()
 
 
+@pytest.mark.parametrize("stages", [1, 2, 3, 4, 7])
+def test_large_tiles_of_few_stages(stages):
+    """The first stages of the largest tiles, when their loads are the farthest behind: operands
+    of small whole numbers, whose sums are exact, that no cache holds any more. What reads a
+    stage before its last load has landed gives another sum."""
+    T = H = 4096
+    K = 64 * stages
+    g = torch.Generator(device="cuda").manual_seed(stages)
+    sets = [tuple(torch.randint(-2, 3, (1, n, K), generator=g, device="cuda").to(F16) for n in (T, H)) for _ in range(4)]
+    flush = torch.empty(1 << 28, dtype=torch.float32, device="cuda")
+    for i, (a, w) in enumerate(sets):
+        _say(f"few stages {stages}, operands {i}")
+        flush.fill_(float(i))
+        y, _ = fc.fc_linear_act(a, w)
+        # whole numbers of at most 4 * 448 < 2048: exact in binary32 and in fp16
+        assert torch.equal(y[0].float(), a[0].float() @ w[0].float().T)
+
+
 LARGE_WEIGHTS = [(200, 4096, 4096, 128), (72, 2816, 8192, 88), (130, 8192, 2816, 64), (65, 4104, 4096, 24), (40000, 64, 512, 64),
                  (5000, 512, 520, 8), (300, 2048, 2048, 32), (9000, 1024, 300, 16), (9000, 1032, 304, 24)]
 
