@@ -64,15 +64,16 @@ __device__ __forceinline__ void load_vector(const LayerNormBackArgs &a, uint64_t
     }
 }
 
-// n of the vector, (x - mean) * rstd as one fma of x, or of the codes (each a
-// subnormal half: a code and its position scaled by 2^-24, as in dequant8).
+// n of the vector: (x - mean) * rstd of 16-bit x, the difference first, so that n keeps its
+// digits where the mean is far above the deviations. Codes take one fma, of q * s and of
+// z - mean, which is in a group's range too (each code is a subnormal half: a code and its
+// position scaled by 2^-24, as in dequant8).
 template <int DT, int SRC>
 __device__ __forceinline__ void normed(const Loaded<SRC> &o, float mean, float rstd, float (&n)[kLaneElems]) {
     if constexpr (SRC == 0) {
-        const float c = -mean * rstd;
         widen8<DT>(o.x, n);
 #pragma unroll
-        for (int k = 0; k < kLaneElems; ++k) n[k] = __builtin_fmaf(n[k], rstd, c);
+        for (int k = 0; k < kLaneElems; ++k) n[k] = (n[k] - mean) * rstd;
     } else {
         const float sc = half_bits_to_float(o.s) * rstd * 16777216.0f;
         const float c = (half_bits_to_float(o.z) - mean) * rstd;
