@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "fc_device.h"
+#include "fc_grid.h"
 #include "fc_launch.h"
 
 namespace fc {
@@ -211,7 +212,7 @@ hipError_t launch_rt(const uint16_t *x, int R, uint64_t n, int g_shift, uint8_t 
                      const uint16_t *res, uint16_t *out, hipStream_t stream) {
     constexpr uint64_t per_block = (uint64_t)kWavesPerBlock * kSlotElems;
     const uint64_t blocks = (n + per_block - 1) / per_block;
-    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    if (!launch_fits(blocks, kBlockThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((allreduce_small_kernel<DT, BITS1, BITS2, RES, RT>), dim3((unsigned)blocks),
                        dim3(kBlockThreads), 0, stream, x, R, n, g_shift, codes1, s1, z1, codes2, s2,
                        z2, res, out);

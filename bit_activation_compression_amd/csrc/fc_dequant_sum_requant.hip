@@ -18,6 +18,7 @@
 // operand), so for R = 4 the kernel is bound by vector ALU issue rather than
 // by HBM; its layout is chosen to keep the instructions per element low.
 #include "fc_device.h"
+#include "fc_grid.h"
 #include "fc_launch.h"
 
 namespace fc {
@@ -308,7 +309,7 @@ hipError_t launch_one(const uint8_t *codes1, const uint16_t *s1, const uint16_t 
     constexpr uint64_t per_block =
         (uint64_t)kK2Waves * (G2 > kWaveRun ? G2 : kWaveRun);
     const uint64_t blocks = (n + per_block - 1) / per_block;
-    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    if (!launch_fits(blocks, kK2Threads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((dsr_kernel<BITS1, BITS2, G2, RT>), dim3((unsigned)blocks), dim3(kK2Threads),
                        0, stream, codes1, s1, z1, R, n, g1_shift, codes2, s2, z2);
     return hipGetLastError();

@@ -12,6 +12,7 @@
 // the dequantize and a separate 16-bit add give, without the round trip of
 // the all-reduce result through HBM (2 more bytes read per element).
 #include "fc_device.h"
+#include "fc_grid.h"
 #include "fc_launch.h"
 
 namespace fc {
@@ -84,7 +85,7 @@ hipError_t launch_one(const uint8_t *codes, const uint16_t *s, const uint16_t *z
                       int g_shift, const uint16_t *res, uint16_t *out, hipStream_t stream) {
     constexpr uint64_t per_block = (uint64_t)kWavesPerBlock * kSlots * kSlotElems;
     const uint64_t blocks = (n + per_block - 1) / per_block;
-    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    if (!launch_fits(blocks, kBlockThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((dequant_kernel<DT, BITS, RES>), dim3((unsigned)blocks), dim3(kBlockThreads),
                        0, stream, codes, s, z, n, g_shift, res, out);
     return hipGetLastError();
@@ -95,11 +96,17 @@ hipError_t launch_any(const uint8_t *codes2, const uint16_t *s2, const uint16_t 
                       int bits, int group2, int dtype, const uint16_t *res, uint16_t *out,
                       hipStream_t stream) {
     const int sh = ilog2(group2);
-    if (dtype == 0)
-        return bits == 4 ? launch_one<0, 4, RES>(codes2, s2, z2, n, sh, res, out, stream)
-                         : launch_one<0, 8, RES>(codes2, s2, z2, n, sh, res, out, stream);
-    return bits == 4 ? launch_one<1, 4, RES>(codes2, s2, z2, n, sh, res, out, stream)
-                     : launch_one<1, 8, RES>(codes2, s2, z2, n, sh, res, out, stream);
+    // 32 values to a thread; pieces of whole groups and of aligned scales
+    return in_pieces(n, uint64_t(1) << 34, (uint64_t)group2 * 8, [&](uint64_t at, uint64_t m) {
+        const uint64_t g = at >> sh;
+        const uint8_t *c = codes2 + at * (uint64_t)bits / 8;
+        const uint16_t *r = RES ? res + at : nullptr;
+        if (dtype == 0)
+            return bits == 4 ? launch_one<0, 4, RES>(c, s2 + g, z2 + g, m, sh, r, out + at, stream)
+                             : launch_one<0, 8, RES>(c, s2 + g, z2 + g, m, sh, r, out + at, stream);
+        return bits == 4 ? launch_one<1, 4, RES>(c, s2 + g, z2 + g, m, sh, r, out + at, stream)
+                         : launch_one<1, 8, RES>(c, s2 + g, z2 + g, m, sh, r, out + at, stream);
+    });
 }
 
 }  // namespace

@@ -29,6 +29,7 @@
 // compiled without the second, whose registers would otherwise set theirs
 // (measured: K1 41 -> 35 us at g = 160; K2 59 -> 34 us at g = 6144).
 #include "fc_device.h"
+#include "fc_grid.h"
 #include "fc_launch.h"
 
 namespace fc {
@@ -764,7 +765,7 @@ hipError_t grid_for(const UnitMap &m, uint64_t groups, unsigned *blocks, uint32_
     const uint64_t per_wave = m.wide ? 1 : (uint64_t)(kWave >> m.p2_shift) * sets;
     const uint64_t waves = (groups + per_wave - 1) / per_wave;
     const uint64_t b = (waves + kWavesPerBlock - 1) / kWavesPerBlock;
-    if (b > 0x7FFFFFFFull || b == 0) return hipErrorInvalidConfiguration;
+    if (!launch_fits(b, kBlockThreads)) return hipErrorInvalidConfiguration;
     *blocks = (unsigned)b;
     return hipSuccess;
 }
@@ -854,18 +855,16 @@ void go_dequant(bool oct, dim3 grid, hipStream_t stream, const uint8_t *codes2,
                            stream, codes2, s2, z2, n, D2, residual, out);
 }
 
-}  // namespace
-
 // M = 0 selects the 2-value units
-hipError_t launch_quantize_generic(const uint16_t *x, int dtype, uint64_t n, int bits, int group,
-                                   uint8_t *codes, uint16_t *s, uint16_t *z, hipStream_t stream) {
+hipError_t quantize_piece(const uint16_t *x, int dtype, uint64_t n, int bits, int group, uint8_t *codes,
+                          uint16_t *s, uint16_t *z, hipStream_t stream) {
     const uint32_t G = (uint32_t)group;
     const int M = G % kLaneElems == 0 ? unit_vectors(G) : 0;
     const UnitMap m = unit_map(G, M ? M * kLaneElems : 2);
     const uint64_t groups = n / G;
     if (M == 0 && G <= kLaneGroupMax) {
         const uint64_t b = (groups + (uint64_t)kWave * kWavesPerBlock - 1) / ((uint64_t)kWave * kWavesPerBlock);
-        if (b > 0x7FFFFFFFull || b == 0) return hipErrorInvalidConfiguration;
+        if (!launch_fits(b, kBlockThreads)) return hipErrorInvalidConfiguration;
         const dim3 grid((unsigned)b);
         if (dtype == 0) {
             if (bits == 4)
@@ -891,6 +890,40 @@ hipError_t launch_quantize_generic(const uint16_t *x, int dtype, uint64_t n, int
     return ok ? hipGetLastError() : hipErrorInvalidValue;
 }
 
+hipError_t dequantize_piece(const uint8_t *codes2, const uint16_t *s2, const uint16_t *z2, uint64_t n,
+                            int bits, int group2, int dtype, const uint16_t *residual, uint16_t *out,
+                            hipStream_t stream) {
+    const bool oct = group2 % kLaneElems == 0;
+    const uint64_t lanes = oct ? n / kLaneElems : (n + 2 * kDqPairs - 1) / (2 * kDqPairs);
+    const uint64_t b = (lanes + kBlockThreads - 1) / kBlockThreads;
+    if (!launch_fits(b, kBlockThreads)) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)b);
+    const GroupDiv D2 = group_div((uint32_t)group2, n);
+#define FC_GO(DT, B, RS) go_dequant<DT, B, RS>(oct, grid, stream, codes2, s2, z2, n, D2, residual, out)
+    const bool res = residual != nullptr;
+    if (dtype == 0) {
+        if (bits == 4) { if (res) FC_GO(0, 4, true); else FC_GO(0, 4, false); }
+        else { if (res) FC_GO(0, 8, true); else FC_GO(0, 8, false); }
+    } else {
+        if (bits == 4) { if (res) FC_GO(1, 4, true); else FC_GO(1, 4, false); }
+        else { if (res) FC_GO(1, 8, true); else FC_GO(1, 8, false); }
+    }
+#undef FC_GO
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_generic(const uint16_t *x, int dtype, uint64_t n, int bits, int group,
+                                   uint8_t *codes, uint16_t *s, uint16_t *z, hipStream_t stream) {
+    // at most a thread to each value, 64 to a long group; pieces of whole groups and of
+    // aligned codes and scales
+    return in_pieces(n, uint64_t(1) << 31, (uint64_t)group * 16, [&](uint64_t at, uint64_t m) {
+        const uint64_t g = at / (uint64_t)group;
+        return quantize_piece(x + at, dtype, m, bits, group, codes + at * (uint64_t)bits / 8, s + g, z + g, stream);
+    });
+}
+
 hipError_t launch_dsr_generic(const uint8_t *codes1, const uint16_t *s1, const uint16_t *z1, int R,
                               uint64_t n, int bits1, int bits2, int group1, int group2,
                               uint8_t *codes2, uint16_t *s2, uint16_t *z2, hipStream_t stream) {
@@ -903,7 +936,7 @@ hipError_t launch_dsr_generic(const uint8_t *codes1, const uint16_t *s1, const u
     const GroupDiv D1 = group_div(G1, n);
     if (M == 0 && same && G2 <= kLaneGroupMax) {
         const uint64_t b = (groups + (uint64_t)kWave * kWavesPerBlock - 1) / ((uint64_t)kWave * kWavesPerBlock);
-        if (b > 0x7FFFFFFFull || b == 0) return hipErrorInvalidConfiguration;
+        if (!launch_fits(b, kBlockThreads)) return hipErrorInvalidConfiguration;
 #define FC_LANE(B1, B2)                                                                                \
     hipLaunchKernelGGL((dsr_lane_kernel<B1, B2>), dim3((unsigned)b), dim3(kBlockThreads), 0, stream, \
                        codes1, s1, z1, R, n, per_op, groups, G2, codes2, s2, z2)
@@ -932,23 +965,12 @@ hipError_t launch_dsr_generic(const uint8_t *codes1, const uint16_t *s1, const u
 hipError_t launch_dequantize_generic(const uint8_t *codes2, const uint16_t *s2, const uint16_t *z2,
                                      uint64_t n, int bits, int group2, int dtype,
                                      const uint16_t *residual, uint16_t *out, hipStream_t stream) {
-    const bool oct = group2 % kLaneElems == 0;
-    const uint64_t lanes = oct ? n / kLaneElems : (n + 2 * kDqPairs - 1) / (2 * kDqPairs);
-    const uint64_t b = (lanes + kBlockThreads - 1) / kBlockThreads;
-    if (b > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)b);
-    const GroupDiv D2 = group_div((uint32_t)group2, n);
-#define FC_GO(DT, B, RS) go_dequant<DT, B, RS>(oct, grid, stream, codes2, s2, z2, n, D2, residual, out)
-    const bool res = residual != nullptr;
-    if (dtype == 0) {
-        if (bits == 4) { if (res) FC_GO(0, 4, true); else FC_GO(0, 4, false); }
-        else { if (res) FC_GO(0, 8, true); else FC_GO(0, 8, false); }
-    } else {
-        if (bits == 4) { if (res) FC_GO(1, 4, true); else FC_GO(1, 4, false); }
-        else { if (res) FC_GO(1, 8, true); else FC_GO(1, 8, false); }
-    }
-#undef FC_GO
-    return hipGetLastError();
+    // 8 values to a thread
+    return in_pieces(n, uint64_t(1) << 34, (uint64_t)group2 * 16, [&](uint64_t at, uint64_t m) {
+        const uint64_t g = at / (uint64_t)group2;
+        return dequantize_piece(codes2 + at * (uint64_t)bits / 8, s2 + g, z2 + g, m, bits, group2, dtype,
+                                residual != nullptr ? residual + at : nullptr, out + at, stream);
+    });
 }
 
 }  // namespace fc

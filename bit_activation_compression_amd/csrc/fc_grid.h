@@ -22,6 +22,24 @@ inline dim3 grid_of_blocks(uint64_t blocks) {
     return blocks <= row ? dim3((unsigned)blocks) : dim3((unsigned)row, (unsigned)((blocks + row - 1) / row));
 }
 
+// Whether a launch of `blocks` workgroups along x counts its threads in 32 bits: what is
+// past that is not refused by the runtime, a launch of 2^32 + n threads runs n of them.
+inline bool launch_fits(uint64_t blocks, unsigned threads) {
+    return blocks != 0 && blocks <= 0xFFFFFFFFull / threads;
+}
+
+// run(first value, values) for n values in pieces of at most `most`, but at least `unit`,
+// which every piece but the last is a multiple of.
+template <class Run>
+hipError_t in_pieces(uint64_t n, uint64_t most, uint64_t unit, Run &&run) {
+    const uint64_t piece = most > unit ? most / unit * unit : unit;
+    for (uint64_t at = 0; at < n; at += piece) {
+        const hipError_t err = run(at, n - at < piece ? n - at : piece);
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+}
+
 // Compute units of the current device (persistent kernels have a workgroup or
 // two on each), looked up once per device. The cache is atomic: calls from
 // several host threads may fill it at once (with the same value).

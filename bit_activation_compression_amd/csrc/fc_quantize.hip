@@ -10,6 +10,7 @@
 // HBM-bound: per element it reads 2 bytes and writes bits/8 bytes, plus
 // 4 bytes of scale and zero per group.
 #include "fc_device.h"
+#include "fc_grid.h"
 #include "fc_launch.h"
 
 namespace fc {
@@ -66,7 +67,7 @@ hipError_t launch_one(const uint16_t *x, uint64_t n, uint8_t *codes, uint16_t *s
                       hipStream_t stream) {
     constexpr uint64_t per_block = (uint64_t)kWavesPerBlock * tile_slots(G, kTileSlots) * kSlotElems;
     const uint64_t blocks = (n + per_block - 1) / per_block;
-    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    if (!launch_fits(blocks, kBlockThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((quantize_kernel<DT, BITS, G>), dim3((unsigned)blocks), dim3(kBlockThreads), 0,
                        stream, x, n, codes, s, z);
     return hipGetLastError();
@@ -89,12 +90,16 @@ hipError_t dispatch_group(const uint16_t *x, uint64_t n, int group, uint8_t *cod
 
 hipError_t launch_quantize(const uint16_t *x, int dtype, uint64_t n, int bits, int group,
                            uint8_t *codes, uint16_t *s, uint16_t *z, hipStream_t stream) {
-    if (dtype == 0) {
-        return bits == 4 ? dispatch_group<0, 4>(x, n, group, codes, s, z, stream)
-                         : dispatch_group<0, 8>(x, n, group, codes, s, z, stream);
-    }
-    return bits == 4 ? dispatch_group<1, 4>(x, n, group, codes, s, z, stream)
-                     : dispatch_group<1, 8>(x, n, group, codes, s, z, stream);
+    // at least 8 values to a thread; pieces of whole groups and of aligned scales
+    return in_pieces(n, uint64_t(1) << 34, (uint64_t)group * 8, [&](uint64_t at, uint64_t m) {
+        const uint64_t g = at / (uint64_t)group;
+        uint8_t *c = codes + at * (uint64_t)bits / 8;
+        if (dtype == 0)
+            return bits == 4 ? dispatch_group<0, 4>(x + at, m, group, c, s + g, z + g, stream)
+                             : dispatch_group<0, 8>(x + at, m, group, c, s + g, z + g, stream);
+        return bits == 4 ? dispatch_group<1, 4>(x + at, m, group, c, s + g, z + g, stream)
+                         : dispatch_group<1, 8>(x + at, m, group, c, s + g, z + g, stream);
+    });
 }
 
 }  // namespace fc

@@ -22,6 +22,7 @@
 #include <stdint.h>
 
 #include "fc_device.h"
+#include "fc_grid.h"
 #include "fc_internal.h"
 
 namespace fc {
@@ -100,14 +101,14 @@ hipError_t launch(const void *src, void *dst, uint64_t n, hipStream_t stream) {
     if constexpr (KIND == 3) {
         constexpr uint64_t per_block = (uint64_t)kWavesPerBlock * U * kWave * 4;
         const uint64_t blocks = (n + per_block - 1) / per_block;
-        if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+        if (!launch_fits(blocks, kBlockThreads)) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((expand_kernel<U>), dim3((unsigned)blocks), dim3(kBlockThreads), 0,
                            stream, static_cast<const uint8_t *>(src), static_cast<uint8_t *>(dst), n);
         return hipGetLastError();
     }
     constexpr uint64_t per_block = (uint64_t)kWavesPerBlock * U * kWave * 16;
     const uint64_t blocks = (n + per_block - 1) / per_block;
-    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    if (!launch_fits(blocks, kBlockThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((stream_kernel<KIND, U>), dim3((unsigned)blocks), dim3(kBlockThreads), 0,
                        stream, static_cast<const uint8_t *>(src), static_cast<uint8_t *>(dst), n);
     return hipGetLastError();

@@ -5,6 +5,7 @@
 //
 // HBM-bound: per output element it reads R 16-bit values and writes one.
 #include "fc_device.h"
+#include "fc_grid.h"
 #include "fc_launch.h"
 
 namespace fc {
@@ -78,7 +79,7 @@ template <int DT, int RT>
 hipError_t launch_one(const uint16_t *x, int R, uint64_t n, uint16_t *out, hipStream_t stream) {
     constexpr uint64_t per_block = (uint64_t)kWavesPerBlock * kSumSlots * kSlotElems;
     const uint64_t blocks = (n + per_block - 1) / per_block;
-    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    if (!launch_fits(blocks, kBlockThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((sum_kernel<DT, RT>), dim3((unsigned)blocks), dim3(kBlockThreads), 0, stream, x, R,
                        n, out);
     return hipGetLastError();
