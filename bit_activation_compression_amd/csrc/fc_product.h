@@ -97,7 +97,7 @@ __device__ __forceinline__ void load_to_lds(const u32x4 &res, uint8_t FC_LDS *to
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"((uint32_t)(uintptr_t)to), "v"(off), "s"(res), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // A dword per lane to LDS the same way.
@@ -105,7 +105,7 @@ __device__ __forceinline__ void touch_to_lds(const u32x4 &res, uint8_t FC_LDS *t
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"((uint32_t)(uintptr_t)to), "v"(off), "s"(res)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 struct ProductArgs {
