@@ -1,5 +1,6 @@
 """More of the training operators on the GPU: the RMS norm's backward pass from payloads,
-with and without the skip connection's gradient, in every kernel that reads them."""
+with and without the skip connection's gradient, in every kernel that reads them; and calls
+with workspaces that run on two streams at a time."""
 from __future__ import annotations
 
 import sys
@@ -52,3 +53,58 @@ def test_backward_from_payload_rms_and_skip(T, H, group, rms, dres, dt):
         over = fc.fc_layer_norm_backward(*args, rms=rms, dres=skip, dx=skip)
         for a, b in zip(got, over):
             assert torch.equal(a, b)
+
+
+def test_two_streams_at_a_time():
+    """Each stream has its own operands, outputs and workspaces, all made beforehand: the host
+    only enqueues, far faster than the calls run, so that those of both streams overlap. Calls
+    that split sums over workgroups, with workspaces that hold the other calls' leftovers."""
+    R, T, K, H = 1, 4096, 1024, 1280
+    g = torch.Generator(device="cuda").manual_seed(6)
+
+    def n(*shape, dt=BF16):
+        return torch.randn(shape, generator=g, device="cuda").to(dt)
+
+    def one():
+        d = dict(dy=n(R, T, H), x=n(T, K), w=n(R, H, K), b=n(R, H), few=n(R, 40, K), rows=n(T, K), pre=n(R, T, H))
+        d["payload"] = fc.fc_quantize_groups(n(R, T, K), 8, 64)
+        d["pz"] = fc.fc_quantize_groups(d["pre"], 8, 32)
+        out = dict(y=n(R, 40, H), dx=n(R, 40, K), dw=n(R, H, K, dt=torch.float32), dz=n(R, T, H), db=n(R, H, dt=torch.float32),
+                   dn=n(T, K), dg=n(K, dt=torch.float32), dbeta=n(K, dt=torch.float32))
+        need = [fc.fc_linear_act_workspace_bytes(R, 40, K, H), fc.fc_linear_input_grad_workspace_bytes(R, 40, K, H),
+                fc.fc_linear_weight_grad_workspace_bytes(R, T, K, H), fc.fc_activation_backward_workspace_bytes(R, T, H),
+                fc.fc_layer_norm_backward_workspace_bytes(T, K)]
+        assert min(need) > 0
+        ws = torch.full((max(need),), 0x7F, dtype=torch.uint8, device="cuda")
+        _, mean, rstd, _ = fc.fc_layer_norm(d["x"], stats=True)
+        small, gain = d["dy"][:, :40].contiguous(), d["x"][0].clone()
+
+        def calls(stream):
+            kw = dict(workspace=ws, stream=stream)
+            fc.fc_linear_act(d["few"], d["w"], d["b"], "gelu", y=out["y"], **kw)
+            fc.fc_linear_input_grad(small, d["w"], dx=out["dx"], **kw)
+            fc.fc_linear_weight_grad(d["dy"], d["payload"], dw=out["dw"], **kw)
+            fc.fc_activation_backward(d["dy"], "silu", d["pz"], dz=out["dz"], db=out["db"], **kw)
+            fc.fc_layer_norm_backward(d["rows"], d["x"], mean, rstd, gain, dx=out["dn"], dw=out["dg"],
+                                      db=out["dbeta"], **kw)
+        return calls, out
+
+    sides = [one(), one()]
+    want = []
+    for calls, out in sides:
+        calls(None)
+        torch.cuda.synchronize()
+        want.append({k: v.clone() for k, v in out.items()})
+    streams = [torch.cuda.Stream() for _ in sides]
+    for turn in range(8):
+        for _, out in sides:
+            for t in out.values():
+                t.fill_(3.0)
+        torch.cuda.synchronize()
+        for _ in range(12):
+            for (calls, _), s in zip(sides, streams):
+                calls(s)
+        torch.cuda.synchronize()
+        for (_, out), w in zip(sides, want):
+            for k, v in out.items():
+                assert torch.equal(v, w[k]), (turn, k)
