@@ -20,7 +20,8 @@
  * layouts. Calls on different streams are independent of each other. An output may
  * not overlap an input or another output (FC_ERR_OVERLAP) except where a call says
  * so. With T == 0 nothing is written, and pointers may be NULL, but for gradients
- * that are sums over tokens: those are zeros then (or stay, where they accumulate).
+ * that are sums over tokens: those are zeros then (or stay, where they accumulate; the
+ * weight gradient's dw is not NULL in any call).
  *
  * Sums, statistics and sums' partial results are binary32, in an order that the
  * call's sizes fix: the same call gives the same bits. NaN and infinities of 16-bit
