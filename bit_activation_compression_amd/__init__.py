@@ -853,7 +853,8 @@ def fc_linear_act(a: torch.Tensor, w: torch.Tensor, bias=None, act: str = "none"
     """a [R, T, K] times w [R, H, K] (or both without R; fp16/bf16) -> (y, z):
         z = a w^T + bias,  y = act(z) * mul + residual
     with bias [R, H], mul and residual [R, T, H]. z is rounded and returned where a tensor (or
-    True, to allocate one) is passed, else None. `y` may be `residual`. act: ACTIVATIONS."""
+    True, to allocate one) is passed, else None. `y` may be `residual`. act: ACTIVATIONS; what
+    act "none" with mul computes has no backward call."""
     R, T, K, H, Kw = _product(a, w, "a")
     if K != Kw:
         raise ValueError("a must be [R, T, K] and w [R, H, K]")

@@ -64,12 +64,11 @@ __device__ __forceinline__ float act_value(float z) {
     } else if constexpr (ACT == kActGelu) {
         float bell;
         return z * normal_cdf(z, bell);
-    } else if constexpr (ACT == kActGeluTanh) {
+    } else {
+        static_assert(ACT == kActGeluTanh, "an activation");
         float p, q;
         sigmoid_pair(gelu_tanh_argument(z), p, q);
         return z * p;
-    } else {
-        return z;
     }
 }
 
@@ -89,14 +88,12 @@ __device__ __forceinline__ void act_both(float z, float &value, float &slope) {
         const float cdf = normal_cdf(z, bell);
         value = z * cdf;
         slope = __builtin_fmaf(z * bell, 0.39894228f, cdf);
-    } else if constexpr (ACT == kActGeluTanh) {
+    } else {
+        static_assert(ACT == kActGeluTanh, "an activation");
         float p, q;
         sigmoid_pair(gelu_tanh_argument(z), p, q);
         value = z * p;
         slope = __builtin_fmaf(value * q, __builtin_fmaf(z * z, 3.0f * 1.59576912f * 0.044715f, 1.59576912f), p);
-    } else {
-        value = z;
-        slope = 1.0f;
     }
 }
 

@@ -97,7 +97,8 @@ size_t fc_layer_norm_backward_workspace_bytes(int T, int H);
  *   a [R][T][K], w [R][H][K], bias [R][H], mul, residual [R][T][H], all in dt -> y
  *   [R][T][H] in dt; z_out [R][T][H] in dt: z rounded, what the activation's backward
  *   pass needs a payload of. bias, mul, residual and z_out are optional (NULL). y may
- *   be the same pointer as residual.
+ *   be the same pointer as residual. FC_ACT_NONE with mul (y = z * mul + residual) has no
+ *   backward call here: fc_activation_backward takes a second factor with an activation.
  * Any sizes with R, K, H >= 1, K, H <= 2^22 and R * ceil(T/16) * ceil(H/16) < 2^31;
  * rows that are whole 16-byte vectors (K % 8 == 0) are faster. workspace:
  * fc_linear_act_workspace_bytes(R, T, K, H) bytes (0 and NULL allowed where the sums
@@ -151,7 +152,8 @@ size_t fc_linear_weight_grad_workspace_bytes(int R, int T, int K, int H);
  *   factor, in the same groups, NULL for none (dmul must then be NULL) -> dz, dmul
  *   [R][T][H] in dt (dz may be dy), db [R][H] binary32 (optional).
  * act == FC_ACT_NONE: the bias gradient of a layer without an activation, db =
- * sum_t dy; payloads, dz and dmul must be NULL, db not, and H is any up to 2^22.
+ * sum_t dy; payloads, dz and dmul must be NULL, db not (FC_ERR_VALUE: a second factor
+ * without an activation has no call here), and H is any up to 2^22.
  * The slope of relu at 0 is 0. workspace:
  * fc_activation_backward_workspace_bytes(R, T, H) bytes where db is asked for (0 and
  * NULL allowed where the tokens are not split).

@@ -1,7 +1,9 @@
 """Limits of the training operators (include/fc/train.h) that their documentation states,
 without a GPU."""
+import pytest
+
 import bit_activation_compression_amd as fc
-from test_train_cpu import P, _weight_grad
+from test_train_cpu import NONE, P, _act, _linear, _weight_grad
 
 
 def test_a_weight_gradient_is_never_null():
@@ -9,6 +11,13 @@ def test_a_weight_gradient_is_never_null():
     none = dict(T=0, dy=None, codes=None, s=None, z=None)
     assert _weight_grad(**none, acc=0, dw=None) == 1 and _weight_grad(**none, acc=1, dw=None) == 1
     assert _weight_grad(**none, acc=1) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(mc=P(4), ms=P(5), mz=P(6)), dict(dmul=P(8)), dict(dz=P(7)),
+                                dict(codes=P(1), s=P(2), z=P(3), mc=P(4), ms=P(5), mz=P(6), dz=P(7), dmul=P(8))])
+def test_a_second_factor_without_an_activation_is_forward_only(kw):
+    assert _linear(act=0, a=None) == 1          # the forward layer takes it: a NULL operand is what it refuses
+    assert _act(**dict(NONE, **kw)) == 10
 
 
 def test_workspaces_of_split_sums():
