@@ -320,16 +320,7 @@ __global__ __launch_bounds__(kColWaves * kWave) void layer_norm_columns_kernel(c
     float dw[kLaneElems] = {}, db[kLaneElems] = {};
     for (uint64_t row = (uint64_t)part * kColWaves + (uint32_t)wave; row < (uint64_t)a.T; row += (uint64_t)parts * kColWaves) {
         Loaded<SRC> o;
-        const uint64_t at = row * (uint64_t)H;
-        o.dy = load_row8(a.dy + at, b, H);
-        if constexpr (SRC == 0) {
-            o.x = load_row8(a.x + at, b, H);
-        } else {
-            o.q = *reinterpret_cast<const u32x2 *>(a.px.codes + at + (uint32_t)b);
-            const uint64_t g = row * (uint64_t)a.groups + group_of((uint32_t)b / kLaneElems, a.gmagic);
-            o.s = a.px.s[g];
-            o.z = a.px.z[g];
-        }
+        load_vector<SRC, false>(a, row, b, o);
         float n[kLaneElems], d[kLaneElems];
         normed<DT, SRC>(o, a.mean != nullptr ? a.mean[row] : 0.0f, a.rstd[row], n);
         widen8<DT>(o.dy, d);

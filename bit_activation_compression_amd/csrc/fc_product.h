@@ -54,10 +54,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_a8 __attribute__((aligned(8)));
 
 #define FC_LDS __attribute__((address_space(3)))
 
@@ -121,14 +119,6 @@ struct ProductArgs {
     LinearEpilogue e;       // 16-bit results
     float *out;             // binary32 results [split][R][M][N]
     int accumulate;
-};
-
-// The memory of one operand's tile: `rows` real rows (of m or n) from the base.
-template <int OP>
-struct Operand {
-    const uint16_t *base;   // kRows: row m0, k 0; kCols: row k 0, column m0
-    uint32_t ld;            // values per memory row
-    int live;               // rows (kRows) or columns (kCols) that exist, from m0
 };
 
 template <int TM, int TN, int WM, int WN, int NS>

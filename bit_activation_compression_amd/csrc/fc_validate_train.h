@@ -22,7 +22,7 @@ inline bool elems_ok(int R, int T, int H) {
     return (uint64_t)R * (uint64_t)T <= kMaxElems / (uint64_t)H;
 }
 
-// Non-NULL and aligned, unless `n` elements are none.
+// Required pointers are there, and all that are there are aligned.
 inline fc_status check_spans(std::initializer_list<Span> required, std::initializer_list<Span> optional) {
     for (const Span &s : required)
         if (s.p == nullptr) return FC_ERR_NULL;
@@ -35,8 +35,9 @@ inline fc_status check_spans(std::initializer_list<Span> required, std::initiali
 
 inline bool dtype_ok(fc_dtype dt) { return dt == FC_F16 || dt == FC_BF16; }
 
-// The sizes of a product: grids of the smallest tile, 16 x 16 outputs, of each of
-// its gradients too.
+// The sizes of a product and of its gradients: blocks of 16 x 16 outputs are counted in 31
+// bits. No workgroup has fewer: the few-token kernel has 16 channels of all its tokens (up to
+// 8), the others tiles of 64 x 64 and more.
 inline fc_status check_product(int R, int T, int K, int H) {
     if (R < 1 || T < 0 || K < 1 || H < 1 || K > kProductMaxSize || H > kProductMaxSize) return FC_ERR_SHAPE;
     const long long tt = ((long long)T + 15) / 16, th = ((long long)H + 15) / 16, tk = ((long long)K + 15) / 16;
