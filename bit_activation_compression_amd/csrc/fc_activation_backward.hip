@@ -8,7 +8,8 @@
 // that db needs no exchange until the share's end: the workgroup's rows meet in
 // LDS, and a second launch adds the shares in a fixed order. Each operand is read
 // once and each output written once: 5 bytes per element (8 with mul), bound by
-// memory: 8192 x 7168 with mul 89 us, 5.3 TB/s; without 55, 5.4; GELU with db 68, 4.4.
+// memory: 8192 x 7168 with mul 83 to 86 us, 5.5 TB/s; without 54, 5.5; GELU 57, with db 66, 4.5
+// (5 of it the second launch); db alone 26, 4.4 (5).
 #include "fc_act.h"
 #include "fc_grid.h"
 #include "fc_launch_train.h"
@@ -21,7 +22,7 @@ constexpr int kShareThreads = 256;   // of a workgroup with a share of the rows
 constexpr int kWholeThreads = 1024;  // of one that has all rows of its columns
 constexpr int kBlocks = 2048;        // workgroups of shares that fill the device
 constexpr int kAhead = 2;            // rows of a lane in flight
-constexpr int kFree = 16384;         // without sums (8192 x 7168, SiLU and mul: 89 us, with 2048 99)
+constexpr int kFree = 16384;         // without sums (8192 x 7168, SiLU and mul, in turn: 89 us, with 2048 99)
 
 template <int DT, int ACT, bool MUL, bool SUMS, int kThreads>
 __global__ __launch_bounds__(kThreads) void activation_back_kernel(const ActBackArgs a) {

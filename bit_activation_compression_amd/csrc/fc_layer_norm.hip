@@ -9,8 +9,9 @@
 // the kernel is bound by memory. The variance is that of x - m (two sums over the
 // row), which keeps its digits where the mean is large.
 //
-// Measured (rotating buffers): 8192 x 8192 bf16 46 us, 5.8 TB/s, with the payload 72,
-// 4.7; 8192 x 4096 fp16 24.6, 5.5, with the payload 38, 4.5; one row of 8192 3.8 us.
+// Measured (rotating buffers): 8192 x 8192 bf16 49 us, 5.5 TB/s, with the payload 65,
+// 5.2; 8192 x 4096 fp16 26, 5.1, with the payload 34.5, 4.9 (its vector instructions take about
+// 70% of the issue slots there); 2048 x 16384 bf16 29, with the payload 36; one row of 8192 2.8.
 //
 // A row of more than 512 elements has a workgroup to itself, thread i holding the
 // vectors of 8 elements i, i + threads, ... Shorter rows lie side by side in a wave,

@@ -14,10 +14,12 @@
 // read twice, the second time mostly from the L2, and leave dw and db to a kernel that
 // reads dy and x by columns.
 //
-// Measured (rotating buffers): 8192 x 8192 bf16 from a payload 85 us, 4.0 TB/s, with dres
-// 99, 4.8; from x 88, 4.6, without dw and db 81; 8192 x 4096 fp16 50 and 52; 1777 x 5003
-// from x 27, its rows aligned to 2 bytes, without dw and db 19; 4096 x 1024 12.5, without
-// 7.2; 2048 x 16384 (read twice) 79, without 48.
+// Measured (rotating buffers that no cache holds, the second launch with it): 8192 x 8192 bf16
+// from a payload 82 us, 4.1 TB/s, with dres 95, 5.0; from x 84, 4.8, with dres 108, without dw
+// and db 78; 8192 x 4096 fp16 49 and 50; 1777 x 5003 from x, its rows aligned to 2 bytes, 27,
+// without dw and db 19; 4096 x 1024 13, without 7; 2048 x 16384 (read twice) 80, without 50, from
+// a payload 75. Vector instructions take half of the issue slots, and no unit is full: a
+// compute unit has one workgroup, whose waves meet once a row.
 #include "fc_grid.h"
 #include "fc_launch_train.h"
 #include "fc_rows.h"
@@ -411,8 +413,11 @@ hipError_t launch_any(LayerNormBackArgs a, hipStream_t stream) {
 bool layer_norm_sums_in_rows(int H) { return H <= kHeldElems; }
 
 // Workgroups whose sums are added up: one for each compute unit (16 waves: the registers
-// hold 20), fewer where there are fewer rows. Two of up to 10 waves were slower where rows
-// are short, for the sums of twice the workgroups: 4096 x 1024 18 against 13 us.
+// hold 20), fewer where there are fewer rows. Two where they fit are slower for the sums of
+// twice the workgroups, us at 256 and at 512: 4096 x 1024 13 and 17, 8192 x 4096 50 and 58, 1777
+// x 5003 27 and 33, 8192 x 5120 54 and 59, 8192 x 6144 64 and 71, 8192 x 8192 84 and 92. Without
+// dw and db they are level but at rows of 10 waves: 1777 x 5003 19.5 and 17.1, 8192 x 5120 53 and
+// 48.
 int layer_norm_parts(int T, int H) {
     if (!layer_norm_sums_in_rows(H)) {
         const int n = (T - 1) / kColWaves + 1;

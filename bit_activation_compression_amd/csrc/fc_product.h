@@ -21,10 +21,11 @@
 // others, and codes, go through registers: loads before a stage's products, stores
 // to LDS after them.
 //
-// Measured (bf16, several runs): linear layer of 8192^3 795 to 858 us (1.28 to 1.38
-// PFLOP/s), 8192 x 8192 x 7168 734 to 793, its input gradient 731 to 741, its weight
-// gradient 840 to 850 with 34 for the values; a library product of the same sizes runs at 1.30 to
-// 1.50, 1.15 to 1.36 (weights by columns) and 1.01 to 1.16 PFLOP/s (both by columns). The
+// Measured (bf16, call by call in turn with a library's product of the same operands, medians
+// of 60, most within 4%): linear layer of 8192^3 867 us against 689, of 8192 x 8192 x 7168 782
+// against 631 (1.23 and 1.52 PFLOP/s), with bias, GELU and z kept 815 against 688 for a product
+// with bias and a GELU of its own; input gradient 782 against 691; weight gradient from codes
+// to binary32 849, 36 of it for the values, against 970 from 16-bit values to 16-bit ones. The
 // matrix cores are busy 61 to 62% of the cycles of a launch of tiles of 256. 32 x 32 x 16
 // instructions ran 8192^3 in 864 us against 834; four waves of 128 x 128 spill (0.72
 // PFLOP/s). The loads to LDS are inline asm: behind the builtin the compiler waits for all
@@ -448,11 +449,11 @@ void product_kernel(const ProductArgs a, uint32_t magic, bool paired) {
         pb = a.b + r * nk + (OPB == kRows ? (uint64_t)(uint32_t)n0 * ldb + k0 : k0 * ldb + (uint32_t)n0);
     }
 
-    // Measured on the linear layer (both operands by rows), with and without, a stage ahead
-    // of the newest staged: 8192 x 8192 x 7168 734 against 759 us, 4096^3 109 against 116,
-    // T = 8192, K = 1024, H = 8192 153 against 163; two and four stages ahead 1 and 2% slower
-    // than one. With an operand by columns it is 3 to 6% slower (whole kilobytes are staged
-    // from neighbouring lines there).
+    // Measured on the linear layer (both operands by rows), with and without in turn, T x K x H,
+    // us: 8192 x 4096 x 14336 784 and 800, 4096^3 117 and 119, 8192 x 1024 x 8192 160 and 167;
+    // 8192^3 848 and 840, 8192 x 8192 x 7168 779 and 776. A stage ahead of the newest staged;
+    // two and four stages ahead 1 and 2% slower than one. With an operand by columns it is 3 to
+    // 6% slower (whole kilobytes are staged from neighbouring lines there).
     constexpr bool kPrefetch = OPA == kRows && OPB == kRows && DIRECT && TM == kLargeTile;
     constexpr bool kThroughRegs = !DIRECT || OPB == kCodes;   // some of a stage goes through registers
     Stager<DT, OPA, TM, S::kWaves, DIRECT> sa;

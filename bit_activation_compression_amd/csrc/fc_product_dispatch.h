@@ -26,7 +26,10 @@ inline long long tile_count(long long n, int tile) { return (n + tile - 1) / til
 // (four stages in LDS); alone on it, or with half of the device idle, they are faster.
 // Measured without the L2 prefetch of linear layers, us at K = N = 4096 and 64 / 512 / 768 / 1024 / 1536 / 2048 / 4096 rows: tiles of
 // 64 25 / 32 / 53 / 68 / 94 / 130 / 245, of 128 54 / 54 / 58 / 72 / 75 / 81 / 158, of 256
-// 86 / 88 / 97 / 108 / 112 / 112 / 115.
+// 86 / 88 / 97 / 108 / 112 / 112 / 115. The ratios stand for every K; all in tiles of 64 / 128 /
+// 256, 8192 rows: N = 4096, K = 64 58 / 39 / 36, K = 320 85 / 58 / 51, K = 1024 158 / 106 / 82,
+// K = 8192 929 / 587 / 432; N = 7168 (the rule has two parts), K = 64 101 / 65 / 68 and 66, K =
+// 320 144 / 95 / 96 and 92.
 inline double tile_cost(long long tiles, int tile, int cus) {
     const double one = tile == kLargeTile ? 0.75 : tile == kMiddleTile ? 0.47 : 0.22;    // half a round or less
     const double full = tile == kLargeTile ? 1.0 : tile == kMiddleTile ? 0.69 : 0.275;   // a round
@@ -93,7 +96,12 @@ inline SplitPlan split_runs(long long K, long long want) {
 
 // Linear layers and input gradients of few outputs: sums over K are split where the
 // tiles of 64 would leave compute units idle. It goes by the sizes alone, so that the
-// workspace (binary32 [split][batches][M][N]) is the same on every device.
+// workspace (binary32 [split][batches][M][N]) is the same on every device. us in one run and
+// as split here, N = 4096, K = 1024 / 1536 / 2048 / 4096: 64 rows 9.5 / 12.1 / 14.8 / 24.9 and
+// 10.5 / 10.6 / 11.6 / 14.6, 128 rows 9.6 / 12.1 / 14.7 / 25.0 and 10.5 / 14.1 / 15.3 / 16.0, 256
+// rows (all of kFill / 2 tiles) 9.7 / 12.3 / 15.0 / 25.3 and 13.4 / 15.4 / 16.8 / 22.9; from
+// there on whole runs are as fast or faster (320 rows, K = 4096 31.5, in two runs 32.4). So
+// sums of 64 stages gain 2 to 10 us, and those of 16 to 32 stages lose 1 to 4 from 128 tiles on.
 inline SplitPlan linear_plan(long long batches, int M, int N, int K) {
     constexpr long long kFill = 512;   // tiles of 64 that fill the device, two on a compute unit
     const long long tiles = batches * tile_count(M, kSmallTile) * tile_count(N, kSmallTile);

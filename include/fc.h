@@ -49,7 +49,9 @@
  * H % R == 0, and the stage-2 group g2 = min(group, H/R) even and dividing
  * H/R. Power-of-two groups in [8, 8192] run on the fast kernels; any other
  * even length (24, 96, 6144, ...) runs on generic kernels with the same
- * bits, more slowly.
+ * bits, more slowly. A reduction or an uncompressed sum whose launch would take
+ * 2^32 threads or more returns FC_ERR_LAUNCH (at the least T * H is past 2^32
+ * then); quantizers and dequantizers go on in further launches.
  */
 #ifndef FC_H_
 #define FC_H_
@@ -68,7 +70,7 @@ typedef enum {
     FC_ERR_BITS = 3,       /* bits is not 4 or 8 */
     FC_ERR_ALIGN = 4,      /* a device pointer is not 16-byte aligned */
     FC_ERR_WORKSPACE = 5,  /* workspace smaller than fc_workspace_bytes() */
-    FC_ERR_LAUNCH = 6,     /* the HIP runtime reported an error at launch */
+    FC_ERR_LAUNCH = 6,     /* the HIP runtime reported an error at launch, or a launch does not fit */
     FC_ERR_DTYPE = 7,      /* dtype is not FC_F16 or FC_BF16 */
     FC_ERR_SCRATCH = 8,    /* the payloads exceed FC_NOALLOC_SCRATCH_BYTES */
     FC_ERR_OVERLAP = 9,    /* an output overlaps another buffer (fc/layer.h) */
