@@ -1,6 +1,7 @@
 """More of the training operators on the GPU: the RMS norm's backward pass from payloads,
-with and without the skip connection's gradient, in every kernel that reads them; and calls
-with workspaces that run on two streams at a time."""
+with and without the skip connection's gradient, in every kernel that reads them; calls with
+workspaces that run on two streams at a time; activations of infinities, NaN and values
+far from zero."""
 from __future__ import annotations
 
 import sys
@@ -108,3 +109,63 @@ def test_two_streams_at_a_time():
         for (_, out), w in zip(sides, want):
             for k, v in out.items():
                 assert torch.equal(v, w[k]), (turn, k)
+
+
+FORMULAS = {"none": lambda z: z, "relu": lambda z: torch.where(z.isnan(), z, z.clamp_min(0)), "silu": lambda z: z / (1 + torch.exp(-z)),
+            # (torch's own normal distribution function is 0 below -8.3)
+            "gelu": lambda z: z * (0.5 * torch.special.erfc(z * -0.5 ** 0.5)),
+            "gelu_tanh": lambda z: z * (1 + torch.tanh((2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3))) / 2}
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("act", list(fc.ACTIVATIONS))
+@pytest.mark.parametrize("T,K", [(2, 64), (40, 72), (40, 4096), (40, 71)])
+def test_activations_of_infinities_nan_and_far_values(T, K, act, dt):
+    """Pre-activations that the bias gives: streamed weights, tiles, split sums, rows of odd length."""
+    far = 3e4 if dt is F16 else 1e30
+    inf, nan = float("inf"), float("nan")
+    bias = torch.tensor([inf, -inf, nan, far, -far, 300.0, -300.0, 90.0, -90.0, 0.0, -0.0, 12.0, -12.0]).to(dt)
+    H = len(bias)
+    a, w = torch.zeros(T, K, dtype=dt, device="cuda"), torch.ones(H, K, dtype=dt, device="cuda")
+    y, z = fc.fc_linear_act(a, w, bias.cuda(), act, z=True)
+    want = FORMULAS[act](bias.double())
+    y, z = y.cpu(), z.cpu()
+    for t in range(T):
+        assert torch.equal(z[t].isnan(), bias.isnan()) and torch.equal(z[t][~bias.isnan()], bias[~bias.isnan()])
+        assert torch.equal(y[t].isnan(), want.isnan()), (y[t], want)
+        ok = ~want.isnan()
+        assert torch.equal(y[t][ok].isinf(), want[ok].isinf()) and torch.equal(y[t][ok].isinf() & (y[t][ok] > 0), want[ok] == inf)
+        fin = torch.isfinite(want)
+        # at |z| = 12 the tails keep their digits (ref.activation); below 1e-36 they are flushed
+        rel = 2e-6 + 6e-7 * bias.double()[fin].clamp(-40, 40) ** 2
+        ref.assert_within(y[t][fin], want[fin], dt, want[fin].abs() * rel + 1e-36, act)
+
+
+@pytest.mark.parametrize("mul", [False, True])
+@pytest.mark.parametrize("act", list(fc.ACTIVATIONS)[1:])
+def test_activation_backward_far_from_zero(act, mul):
+    """Values of a payload up to 1.6e7 on both sides: past 50 the slope is 0 or 1 to within
+    |z| exp(-|z|) < 1e-20, the value 0 or z to within 50 times that."""
+    T, H, group = 5, 64, 8
+    scale = torch.tensor([[1.0, 64.0, 1000.0, 65504.0, 0.5, 8.0, 30000.0, 257.0]]).half().expand(T, H // group).contiguous()
+    zero = -torch.where(scale > 256, torch.full_like(scale, 65504.0), 128 * scale)
+    codes = torch.tensor([0, 1, 2, 3, 252, 253, 254, 255], dtype=torch.uint8).repeat(T, H // 8)
+    payload = (codes, scale.view(torch.uint16), zero.contiguous().view(torch.uint16))
+    z = ref.held(payload, group)
+    keep = z.abs() > 50
+    assert keep.sum() > T * H // 2 and z.max() > 1.5e7
+    dy = torch.randn(T, H, generator=torch.Generator().manual_seed(22)).to(BF16)
+    m = ref.quantized(torch.randn(T, H, generator=torch.Generator().manual_seed(23)).to(BF16), group)
+    dz, dm, _ = fc.fc_activation_backward(dy.cuda(), act, _payload_on(payload), mul=_payload_on(m) if mul else None)
+    factor = ref.held(m, group) if mul else torch.ones_like(z)
+    want = torch.where(z > 0, dy.double() * factor, 0.0)
+    # on the positive side ref.activation's 2e-6, and two products
+    bound = (1e-18 + 2e-6 * (z > 0) + 3 * ref.U * (z > 0)) * (dy.double() * factor).abs()
+    ref.assert_within(dz.cpu()[keep], want[keep], BF16, bound[keep], "dz")
+    if mul:
+        want = dy.double() * z.clamp_min(0)
+        ref.assert_within(dm.cpu()[keep], want[keep], BF16, ((2e-6 + 4 * ref.U) * want.abs() + 1e-18 * dy.double().abs())[keep], "dmul")
+
+
+def _payload_on(payload):
+    return tuple(t.cuda() for t in payload)
