@@ -103,7 +103,7 @@ inline SplitPlan split_runs(long long K, long long want) {
 // there on whole runs are as fast or faster (320 rows, K = 4096 31.5, in two runs 32.4). So
 // sums of 64 stages gain 2 to 10 us, and those of 16 to 32 stages lose 1 to 4 from 128 tiles on.
 inline SplitPlan linear_plan(long long batches, int M, int N, int K) {
-    constexpr long long kFill = 512;   // tiles of 64 that fill the device, two on a compute unit
+    constexpr long long kFill = 512;   // tiles of 64 that fill 256 compute units, two on each
     const long long tiles = batches * tile_count(M, kSmallTile) * tile_count(N, kSmallTile);
     return split_runs(K, tiles <= kFill / 2 ? kFill / tiles : 1);
 }
@@ -122,7 +122,7 @@ struct WeightGradPlan {
 };
 
 inline WeightGradPlan weight_grad_plan(int R, int T, int K, int H) {
-    constexpr long long kFill = 512;   // tiles of 128 that fill the device, two on a compute unit
+    constexpr long long kFill = 512;   // tiles of 128 that fill 256 compute units, two on each
     WeightGradPlan p = {};
     const double work = (double)R * (double)T * (double)K * (double)H;
     if (H >= 512 && H % 8 == 0 && work >= 1e9)
